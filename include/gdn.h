@@ -373,6 +373,172 @@ int gdn_swa_attention(const void *q, const void *k, const void *v, void *o, cons
                       int num_seqs, int64_t total_tokens, int Hq, int Hkv, int d, int window, float scale,
                       int dtype, int32_t *status, void *stream);
 
+/* ------------------------------------------------------------------ drafted trees and a bounded cache
+ *
+ * Decoding with the hybrid block when several continuations are tried at
+ * once, or when the attention layer's memory is kept at a constant size.
+ *
+ * A tree of drafted tokens.  Sequence b brings n_b nodes, packed one sequence
+ * after another like the tokens of gdn_prefill.  parents[t] is the index,
+ * within its sequence, of the node that node t continues, or -1 when it
+ * continues the tokens already seen; several nodes may.  A parent comes before
+ * its children (parents[t] < t's own index); an entry that breaks this is read
+ * as -1.  parents = NULL is a chain: every node continues the one before it,
+ * which is a plain run of tokens, and with one node a decode step.
+ *
+ * A bounded cache.  k_cache, v_cache [num_seqs, capacity, Hkv, d] hold, per
+ * sequence, cache_lens[b] slots (device, int32; read as 0 below 0 and as the
+ * capacity above it).  What lies in the slots from cache_lens[b] on is never
+ * used and may be anything.  Keys are stored as they enter the scores
+ * (rotated).  cache_pos [num_seqs, Hkv, capacity] int32 gives every slot's
+ * token position, per key/value head, once slots no longer hold the tokens in
+ * order (gdn_cache_insert keeps it); seen[b] is the number of tokens the
+ * sequence has seen before this call's.  Without cache_pos slot s is at
+ * position s and seen[b] is cache_lens[b].
+ *
+ * cu_seqlens is as in gdn_prefill throughout (NULL: equal sequences); rows
+ * from cu_seqlens[num_seqs] on are neither read nor written.
+ */
+
+/* Most nodes of one sequence's tree. */
+#define GDN_MAX_TREE_NODES 64
+
+/*
+ * Attention of a tree of drafted tokens over a cache, per sequence:
+ *
+ *   node i sees the cache's slots, itself and its ancestors;
+ *   o[i, h]   = sum_s softmax_s(scale * q[i, h] . k[s, h / (Hq / Hkv)]) v[s, h / (Hq / Hkv)]
+ *   lse[i, h] = log sum_s exp(scale * q[i, h] . k[s, h / (Hq / Hkv)])
+ *
+ * With window > 0 only keys whose position is more than (node's position -
+ * window) count, where a node's position is seen[b] + its number of ancestors
+ * (window includes the node itself, as in gdn_swa_attention).  A node always
+ * sees itself, so no row is empty.
+ *
+ *   q           [total_nodes, Hq, d]   bf16 (rotated)
+ *   k, v        [total_nodes, Hkv, d]  bf16, the nodes' own keys and values (k rotated)
+ *   parents     [total_nodes] int32, or NULL
+ *   k_cache, v_cache  [num_seqs, capacity, Hkv, d] bf16; may be NULL when capacity is 0
+ *   cache_lens  [num_seqs] int32; may be NULL when capacity is 0
+ *   cache_pos   [num_seqs, Hkv, capacity] int32, or NULL; needs seen
+ *   seen        [num_seqs] int32, or NULL (read only with cache_pos and a window)
+ *   o           [total_nodes, Hq, d]   bf16 (written)
+ *   lse         [total_nodes, Hq]      fp32 (written), or NULL
+ *   max_nodes   1 .. GDN_MAX_TREE_NODES: no sequence has more nodes
+ *   window      tokens, or 0 for no window
+ *   scale       > 0, or 0 for 1/sqrt(d)
+ *   workspace   gdn_tree_attention_workspace_size() bytes; its first int32 is
+ *               the status word (gdn_read_status)
+ * Scores, maxima and row sums are fp32; the probabilities enter the product
+ * with v as bf16.  q, k, v and the cached slots must be finite.  Outputs may
+ * not overlap the inputs or each other.  Supported: dtype GDN_BF16, d = 128,
+ * Hq a multiple of Hkv with Hq / Hkv <= 128, num_seqs * capacity and
+ * total_nodes below 2^31 - 256.
+ */
+size_t gdn_tree_attention_workspace_size(int num_seqs, int64_t total_nodes, int max_nodes, int64_t capacity, int Hq,
+                                         int Hkv, int d, int dtype);
+int gdn_tree_attention(const void *q, const void *k, const void *v, const int32_t *parents,
+                       const int32_t *cu_seqlens, const void *k_cache, const void *v_cache,
+                       const int32_t *cache_lens, const int32_t *cache_pos, const int32_t *seen, void *o, float *lse,
+                       int num_seqs, int64_t total_nodes, int max_nodes, int64_t capacity, int Hq, int Hkv, int d,
+                       int window, float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The Gated DeltaNet read-out of every node of a tree, from one state per
+ * sequence and head.  With S_{-1} = state and p the parent of node i:
+ *
+ *   S_i = exp(g_i) S_p (I - beta_i k_i k_i^T) + beta_i v_i k_i^T,   o_i = S_i q_i
+ *
+ * No S_i is formed: the state is read once and left as it is.  When a path of
+ * the tree is accepted, gdn_prefill over its tokens (or gdn_decode_step)
+ * moves the state on.
+ *
+ *   q, k    [total_nodes, H, dk]  dtype;   v  [total_nodes, H, dv]  dtype
+ *   g, beta [total_nodes, H]      fp32
+ *   parents [total_nodes] int32, or NULL
+ *   state   [num_seqs, H, dv, dk] fp32, or NULL for zeros
+ *   out     [total_nodes, H, dv]  dtype (written; may not overlap the inputs)
+ *   max_nodes  1 .. GDN_MAX_TREE_NODES: no sequence has more nodes
+ * The state enters the products in fp32 (GDN_F32) or as the sum of two bf16
+ * numbers (GDN_BF16, relative error 2^-17).  Supported: dk = dv in {64, 128};
+ * dtype GDN_F32 or GDN_BF16.
+ */
+int gdn_tree_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                  const int32_t *parents, const float *state, void *out, const int32_t *cu_seqlens, int num_seqs,
+                  int64_t total_nodes, int max_nodes, int H, int dk, int dv, int dtype, void *stream);
+
+/*
+ * Attention weight received by every slot of a cache, added up.  A call
+ * brings the m_b newest tokens of every sequence (not yet in the cache) and
+ * the queries of the last nq_b <= m_b of them, with the log-sum-exp that
+ * gdn_tree_attention returned for those queries:
+ *
+ *   weights_out[b, kh, s] = weights_in[b, kh, s] + sum over the queries i and the heads h of group kh of
+ *                           exp(scale * q[i, h] . k_cache[b, s, kh] - lse[i, h])
+ *   new_weights[j, kh]    = the same sum over the queries from token j on, with key k[j, kh]
+ *
+ * A query whose lse is -infinity adds nothing.  With a window only keys within
+ * it of the query count (positions as above; token j of a call is at seen[b] +
+ * j).  The sum of a slot runs in a fixed order, so results repeat bit by bit.
+ *
+ *   q            [total_queries, Hq, d]  bf16;   lse  [total_queries, Hq]  fp32
+ *   k            [total_tokens, Hkv, d]  bf16
+ *   k_cache, cache_lens, cache_pos, seen, window, scale   as in gdn_tree_attention
+ *   weights_in   [num_seqs, Hkv, capacity] fp32
+ *   weights_out  the same (written below cache_lens[b] only); may equal weights_in
+ *   new_weights  [total_tokens, Hkv]  fp32 (written)
+ *   cu_queries, cu_tokens   as cu_seqlens, of the queries and of the tokens;
+ *                both NULL, or both given; with more queries than tokens in a
+ *                sequence the last m_b queries count
+ *   workspace    gdn_cache_weights_workspace_size() bytes; its first int32 is
+ *                the status word (gdn_read_status)
+ * Supported: dtype GDN_BF16, d = 128, heads and sizes as in gdn_tree_attention.
+ */
+size_t gdn_cache_weights_workspace_size(int num_seqs, int64_t total_queries, int64_t total_tokens, int64_t capacity,
+                                        int Hq, int Hkv, int d, int dtype);
+int gdn_cache_weights(const void *q, const float *lse, const void *k, const void *k_cache, const float *weights_in,
+                      float *weights_out, float *new_weights, const int32_t *cu_queries, const int32_t *cu_tokens,
+                      const int32_t *cache_lens, const int32_t *cache_pos, const int32_t *seen, int num_seqs,
+                      int64_t total_queries, int64_t total_tokens, int64_t capacity, int Hq, int Hkv, int d,
+                      int window, float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * New tokens enter a cache of constant size; the lightest slots give way.
+ * Per sequence and key/value head, of the cache_lens[b] slots and the m_b new
+ * tokens (in this order) the min(capacity, cache_lens[b] + m_b) best stay:
+ * first those among the last `recent` positions of the stream, then the ones
+ * of greatest weight; of equal weights the earlier in the order.  A NaN weight
+ * counts as less than any other.  Slots that stay are not moved.  The new
+ * tokens that stay go, in order, to the evicted and the empty slots, in
+ * ascending order, with their key, value, weight and position (seen[b] + j).
+ * With recent = capacity the cache holds the last tokens, a sliding window.
+ *
+ *   k, v          [total_tokens, Hkv, d]            dtype
+ *   k_cache, v_cache  [num_seqs, capacity, Hkv, d]  dtype, updated in place
+ *   weights_in, cache_pos_in  [num_seqs, Hkv, capacity]  fp32, int32
+ *   weights_out, cache_pos_out  the same (written below the new length only);
+ *                 each may equal its input
+ *   cache_lens_in, seen_in   [num_seqs] int32
+ *   cache_lens_out, seen_out [num_seqs] int32 (written; the length and
+ *                 the tokens seen afterwards); each may equal its input
+ *   new_weights   [total_tokens, Hkv] fp32, or NULL for zeros
+ *   slots         [total_tokens, Hkv] int32 (written): where each token went,
+ *                 -1 where it did not stay
+ *   recent        0 .. capacity
+ *   workspace     gdn_cache_insert_workspace_size() bytes (may be NULL when
+ *                 that is 0)
+ * Supported: GDN_F32 or GDN_BF16, d * size of dtype a multiple of 16 bytes,
+ * capacity >= 1, num_seqs * Hkv <= 65535, capacity + total_tokens below 2^30.
+ * Apart from the in-place pairs, outputs may not overlap inputs or each other.
+ */
+size_t gdn_cache_insert_workspace_size(int num_seqs, int64_t total_tokens, int64_t capacity, int Hkv, int d, int dtype);
+int gdn_cache_insert(const void *k, const void *v, void *k_cache, void *v_cache, const float *weights_in,
+                     float *weights_out, const int32_t *cache_pos_in, int32_t *cache_pos_out,
+                     const int32_t *cache_lens_in, int32_t *cache_lens_out, const int32_t *seen_in,
+                     int32_t *seen_out, const float *new_weights, int32_t *slots, const int32_t *cu_seqlens,
+                     int num_seqs, int64_t total_tokens, int64_t capacity, int Hkv, int d, int recent, int dtype,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------ streaming session
  *
  * One Gated DeltaNet layer step over a constant-size memory, captured as a

@@ -430,4 +430,242 @@ int gdn_swa_attention(const void *q, const void *k, const void *v, void *o, cons
     return e == cudaSuccess ? GDN_OK : cuda_fail(e);
 }
 
+// ------------------------------------------------------------------ drafted trees and the bounded cache
+
+}  // extern "C"
+
+namespace {
+
+// Sizes that the two attention entry points over a cache share.
+int check_cache_attention(int num_seqs, int64_t rows_q, int64_t rows_k, int64_t capacity, int Hq, int Hkv, int d,
+                          int window, float scale, int dtype) {
+    if (num_seqs < 1 || rows_q < 0 || rows_k < 0 || capacity < 0 || Hq < 1 || Hkv < 1 || window < 0)
+        return GDN_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || Hq > 65535 || num_seqs > 65535) return GDN_ERR_INVALID_ARG;
+    if (!(scale >= 0.f) || !(scale < 3.0e38f)) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    const int64_t most = (int64_t)INT32_MAX - 256;
+    if (rows_q > most || rows_k > most || capacity > most || (int64_t)num_seqs * capacity > most)
+        return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 || d != 128 || Hq / Hkv > 128) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+struct Span {
+    const void *p;
+    size_t n;
+};
+
+// Null or misaligned pointers among the needed ones, misaligned optional ones.
+template <int N> bool bad_pointers(const void *const (&need)[N]) {
+    for (const void *p : need)
+        if (!p || misaligned(p)) return true;
+    return false;
+}
+template <int N> bool bad_optional(const void *const (&opt)[N]) {
+    for (const void *p : opt)
+        if (p && misaligned(p)) return true;
+    return false;
+}
+
+// true if an output shares a byte with an input or with another output
+template <int NO, int NI> bool outputs_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return true;
+        for (int j = i + 1; j < NO; ++j)
+            if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+    }
+    return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_tree_attention_workspace_size(int num_seqs, int64_t total_nodes, int max_nodes, int64_t capacity, int Hq,
+                                         int Hkv, int d, int dtype) {
+    if (check_cache_attention(num_seqs, total_nodes, 0, capacity, Hq, Hkv, d, 0, 0.f, dtype) != GDN_OK) return 0;
+    if (max_nodes < 1 || max_nodes > GDN_MAX_TREE_NODES) return 0;
+    return gdn::tree_attention_workspace();
+}
+
+int gdn_tree_attention(const void *q, const void *k, const void *v, const int32_t *parents,
+                       const int32_t *cu_seqlens, const void *k_cache, const void *v_cache,
+                       const int32_t *cache_lens, const int32_t *cache_pos, const int32_t *seen, void *o, float *lse,
+                       int num_seqs, int64_t total_nodes, int max_nodes, int64_t capacity, int Hq, int Hkv, int d,
+                       int window, float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    const int st = check_cache_attention(num_seqs, total_nodes, 0, capacity, Hq, Hkv, d, window, scale, dtype);
+    if (st != GDN_OK) return st;
+    if (max_nodes < 1 || max_nodes > GDN_MAX_TREE_NODES) return GDN_ERR_INVALID_ARG;
+    if (!cu_seqlens && (total_nodes % num_seqs != 0 || total_nodes / num_seqs > max_nodes)) return GDN_ERR_INVALID_ARG;
+    if (cache_pos && !seen) return GDN_ERR_INVALID_ARG;
+    if (total_nodes == 0) return GDN_OK;
+    const void *need[] = {q, k, v, o};
+    const void *opt[] = {parents, cu_seqlens, k_cache, v_cache, cache_lens, cache_pos, seen, lse, workspace};
+    if (bad_pointers(need) || bad_optional(opt)) return GDN_ERR_INVALID_ARG;
+    if (capacity > 0 && (!k_cache || !v_cache || !cache_lens)) return GDN_ERR_INVALID_ARG;
+    const size_t want = gdn_tree_attention_workspace_size(num_seqs, total_nodes, max_nodes, capacity, Hq, Hkv, d, dtype);
+    if (!workspace || workspace_bytes < want) return GDN_ERR_WORKSPACE;
+    const size_t nq = (size_t)total_nodes * Hq * d * 2, nkv = (size_t)total_nodes * Hkv * d * 2;
+    const size_t slots = (size_t)num_seqs * capacity * Hkv, nb = (size_t)num_seqs * 4;
+    const Span outs[] = {{o, nq}, {lse, (size_t)total_nodes * Hq * 4}, {workspace, want}};
+    const Span ins[] = {{q, nq}, {k, nkv}, {v, nkv}, {parents, (size_t)total_nodes * 4}, {cu_seqlens, nb + 4},
+                        {k_cache, slots * d * 2}, {v_cache, slots * d * 2}, {cache_lens, nb}, {cache_pos, slots * 4},
+                        {seen, nb}};
+    if (outputs_overlap(outs, ins)) return GDN_ERR_INVALID_ARG;
+    gdn::TreeAttnLaunch L;
+    L.q = q; L.k = k; L.v = v;
+    L.parents = parents; L.cu_seqlens = cu_seqlens;
+    L.k_cache = k_cache; L.v_cache = v_cache;
+    L.cache_lens = cache_lens; L.cache_pos = cache_pos; L.seen = seen;
+    L.o = o; L.lse = lse;
+    L.num_seqs = num_seqs; L.total_nodes = total_nodes; L.max_nodes = max_nodes; L.capacity = capacity;
+    L.Hq = Hq; L.Hkv = Hkv; L.window = window;
+    L.scale = scale > 0.f ? scale : 1.f / sqrtf((float)d);
+    L.workspace = workspace;
+    L.timeout_ns = g_wait_limit_ns;
+    L.drain_ns = kWaitLimitNs;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), s);
+    if (e == cudaSuccess) e = gdn::launch_tree_attention(L, s);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+int gdn_tree_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                  const int32_t *parents, const float *state, void *out, const int32_t *cu_seqlens, int num_seqs,
+                  int64_t total_nodes, int max_nodes, int H, int dk, int dv, int dtype, void *stream) {
+    if (num_seqs < 1 || H < 1 || total_nodes < 0) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (max_nodes < 1 || max_nodes > GDN_MAX_TREE_NODES) return GDN_ERR_INVALID_ARG;
+    if (!shape_supported(dk, dv)) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * H > (int64_t)INT32_MAX / 2) return GDN_ERR_INVALID_ARG;
+    if (total_nodes > (int64_t)INT32_MAX) return GDN_ERR_INVALID_ARG;
+    if (!cu_seqlens && (total_nodes % num_seqs != 0 || total_nodes / num_seqs > max_nodes)) return GDN_ERR_INVALID_ARG;
+    if (total_nodes == 0) return GDN_OK;
+    const void *need[] = {q, k, v, g, beta, out};
+    const void *opt[] = {parents, state, cu_seqlens};
+    if (bad_pointers(need) || bad_optional(opt)) return GDN_ERR_INVALID_ARG;
+    const size_t tens = (size_t)total_nodes * H * dk * (dtype == GDN_BF16 ? 2 : 4), gates = (size_t)total_nodes * H * 4;
+    const Span outs[] = {{out, tens}};
+    const Span ins[] = {{q, tens}, {k, tens}, {v, tens}, {g, gates}, {beta, gates}, {parents, (size_t)total_nodes * 4},
+                        {state, (size_t)num_seqs * H * dk * dv * 4}, {cu_seqlens, (size_t)num_seqs * 4 + 4}};
+    if (outputs_overlap(outs, ins)) return GDN_ERR_INVALID_ARG;
+    gdn::TreeStepLaunch L;
+    L.q = q; L.k = k; L.v = v;
+    L.g = g; L.beta = beta;
+    L.parents = parents; L.state = state; L.out = out;
+    L.cu_seqlens = cu_seqlens;
+    L.num_seqs = num_seqs; L.total_nodes = total_nodes; L.max_nodes = max_nodes;
+    L.H = H; L.d = dk; L.dtype = dtype;
+    const cudaError_t e = gdn::launch_tree_step(L, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+size_t gdn_cache_weights_workspace_size(int num_seqs, int64_t total_queries, int64_t total_tokens, int64_t capacity,
+                                        int Hq, int Hkv, int d, int dtype) {
+    if (check_cache_attention(num_seqs, total_queries, total_tokens, capacity, Hq, Hkv, d, 0, 0.f, dtype) != GDN_OK)
+        return 0;
+    return gdn::cache_weights_workspace();
+}
+
+int gdn_cache_weights(const void *q, const float *lse, const void *k, const void *k_cache, const float *weights_in,
+                      float *weights_out, float *new_weights, const int32_t *cu_queries, const int32_t *cu_tokens,
+                      const int32_t *cache_lens, const int32_t *cache_pos, const int32_t *seen, int num_seqs,
+                      int64_t total_queries, int64_t total_tokens, int64_t capacity, int Hq, int Hkv, int d,
+                      int window, float scale, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    const int st = check_cache_attention(num_seqs, total_queries, total_tokens, capacity, Hq, Hkv, d, window, scale, dtype);
+    if (st != GDN_OK) return st;
+    if ((cu_queries != nullptr) != (cu_tokens != nullptr)) return GDN_ERR_INVALID_ARG;
+    if (!cu_queries && (total_queries % num_seqs != 0 || total_tokens % num_seqs != 0)) return GDN_ERR_INVALID_ARG;
+    if (cache_pos && !seen) return GDN_ERR_INVALID_ARG;
+    if (total_tokens == 0 && capacity == 0) return GDN_OK;
+    if (total_queries > 0 && (!q || !lse)) return GDN_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!k || !new_weights)) return GDN_ERR_INVALID_ARG;
+    if (capacity > 0 && (!k_cache || !weights_in || !weights_out || !cache_lens)) return GDN_ERR_INVALID_ARG;
+    const void *opt[] = {q, lse, k, k_cache, weights_in, weights_out, new_weights, cu_queries, cu_tokens, cache_lens,
+                         cache_pos, seen, workspace};
+    if (bad_optional(opt)) return GDN_ERR_INVALID_ARG;
+    const size_t want = gdn_cache_weights_workspace_size(num_seqs, total_queries, total_tokens, capacity, Hq, Hkv, d, dtype);
+    if (!workspace || workspace_bytes < want) return GDN_ERR_WORKSPACE;
+    const size_t nq = (size_t)total_queries * Hq, nk = (size_t)total_tokens * Hkv;
+    const size_t slots = (size_t)num_seqs * capacity * Hkv, nb = (size_t)num_seqs * 4;
+    const Span outs[] = {{weights_out, slots * 4}, {new_weights, nk * 4}, {workspace, want}};
+    const Span ins[] = {{q, nq * d * 2}, {lse, nq * 4}, {k, nk * d * 2}, {k_cache, slots * d * 2},
+                        {weights_out == weights_in ? nullptr : weights_in, slots * 4}, {cu_queries, nb + 4},
+                        {cu_tokens, nb + 4}, {cache_lens, nb}, {cache_pos, slots * 4}, {seen, nb}};
+    if (outputs_overlap(outs, ins)) return GDN_ERR_INVALID_ARG;
+    gdn::CacheWeightsLaunch L;
+    L.q = q; L.lse = lse; L.k = k; L.k_cache = k_cache;
+    L.w_in = weights_in; L.w_out = weights_out; L.w_new = new_weights;
+    L.cu_queries = cu_queries; L.cu_tokens = cu_tokens;
+    L.cache_lens = cache_lens; L.cache_pos = cache_pos; L.seen = seen;
+    L.num_seqs = num_seqs;
+    L.total_queries = total_queries; L.total_tokens = total_tokens; L.capacity = capacity;
+    L.Hq = Hq; L.Hkv = Hkv; L.window = window;
+    L.scale = scale > 0.f ? scale : 1.f / sqrtf((float)d);
+    L.workspace = workspace;
+    L.timeout_ns = g_wait_limit_ns;
+    L.drain_ns = kWaitLimitNs;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), s);
+    if (e == cudaSuccess) e = gdn::launch_cache_weights(L, s);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+static int check_cache_insert(int num_seqs, int64_t total_tokens, int64_t capacity, int Hkv, int d, int dtype) {
+    if (num_seqs < 1 || total_tokens < 0 || capacity < 1 || Hkv < 1 || d < 1) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if ((int64_t)num_seqs * Hkv > 65535 || total_tokens >= (1ll << 30) || capacity >= (1ll << 30) - total_tokens)
+        return GDN_ERR_INVALID_ARG;
+    if (d > 65536 || d % (dtype == GDN_BF16 ? 8 : 4) != 0) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+size_t gdn_cache_insert_workspace_size(int num_seqs, int64_t total_tokens, int64_t capacity, int Hkv, int d, int dtype) {
+    if (check_cache_insert(num_seqs, total_tokens, capacity, Hkv, d, dtype) != GDN_OK) return 0;
+    return gdn::cache_insert_workspace(total_tokens, Hkv);
+}
+
+int gdn_cache_insert(const void *k, const void *v, void *k_cache, void *v_cache, const float *weights_in,
+                     float *weights_out, const int32_t *cache_pos_in, int32_t *cache_pos_out,
+                     const int32_t *cache_lens_in, int32_t *cache_lens_out, const int32_t *seen_in,
+                     int32_t *seen_out, const float *new_weights, int32_t *slots, const int32_t *cu_seqlens,
+                     int num_seqs, int64_t total_tokens, int64_t capacity, int Hkv, int d, int recent, int dtype,
+                     void *workspace, size_t workspace_bytes, void *stream) {
+    const int st = check_cache_insert(num_seqs, total_tokens, capacity, Hkv, d, dtype);
+    if (st != GDN_OK) return st;
+    if (recent < 0 || recent > capacity) return GDN_ERR_INVALID_ARG;
+    if (!cu_seqlens && total_tokens % num_seqs != 0) return GDN_ERR_INVALID_ARG;
+    const void *need[] = {k_cache, v_cache, weights_in, weights_out, cache_pos_in, cache_pos_out, cache_lens_in,
+                          cache_lens_out, seen_in, seen_out};
+    const void *opt[] = {k, v, new_weights, slots, cu_seqlens, workspace};
+    if (bad_pointers(need) || bad_optional(opt)) return GDN_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!k || !v || !slots)) return GDN_ERR_INVALID_ARG;
+    const size_t want = gdn::cache_insert_workspace(total_tokens, Hkv);
+    if (want > 0 && (!workspace || workspace_bytes < want)) return GDN_ERR_WORKSPACE;
+    const size_t rows = (size_t)total_tokens * Hkv, cells = (size_t)num_seqs * capacity * Hkv, nb = (size_t)num_seqs * 4;
+    const size_t rb = (size_t)d * (dtype == GDN_BF16 ? 2 : 4);
+    const Span outs[] = {{k_cache, cells * rb}, {v_cache, cells * rb}, {weights_out, cells * 4}, {cache_pos_out, cells * 4},
+                         {cache_lens_out, nb}, {seen_out, nb}, {slots, rows * 4}, {workspace, want}};
+    const Span ins[] = {{k, rows * rb}, {v, rows * rb}, {weights_out == weights_in ? nullptr : weights_in, cells * 4},
+                        {cache_pos_out == cache_pos_in ? nullptr : cache_pos_in, cells * 4},
+                        {cache_lens_out == cache_lens_in ? nullptr : cache_lens_in, nb},
+                        {seen_out == seen_in ? nullptr : seen_in, nb}, {new_weights, rows * 4}, {cu_seqlens, nb + 4}};
+    if (outputs_overlap(outs, ins)) return GDN_ERR_INVALID_ARG;
+    gdn::CacheInsertLaunch L;
+    L.k = k; L.v = v; L.k_cache = k_cache; L.v_cache = v_cache;
+    L.w_in = weights_in; L.w_out = weights_out;
+    L.pos_in = cache_pos_in; L.pos_out = cache_pos_out;
+    L.lens_in = cache_lens_in; L.lens_out = cache_lens_out;
+    L.seen_in = seen_in; L.seen_out = seen_out;
+    L.w_new = new_weights; L.slots = slots; L.cu_seqlens = cu_seqlens;
+    L.num_seqs = num_seqs; L.total_tokens = total_tokens; L.capacity = capacity;
+    L.Hkv = Hkv; L.recent = recent;
+    L.row_bytes = (int64_t)rb;
+    L.workspace = workspace;
+    const cudaError_t e = gdn::launch_cache_insert(L, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
 }  // extern "C"

@@ -126,4 +126,78 @@ cudaError_t swa_setup();
 cudaError_t launch_rope(int dtype, const void *x, void *out, const int32_t *cu_seqlens, int num_seqs,
                         int64_t total_tokens, int H, int d, int offset, double base, cudaStream_t stream);
 
+// Drafted trees and the bounded cache (tree_attention.cu, tree_step.cu,
+// cache_weights.cu, cache_insert.cu); fields as the arguments in gdn.h.
+struct TreeAttnLaunch {
+    const void *q, *k, *v;
+    const int32_t *parents, *cu_seqlens;
+    const void *k_cache, *v_cache;
+    const int32_t *cache_lens, *cache_pos, *seen;
+    void *o;
+    float *lse;
+    int num_seqs;
+    int64_t total_nodes;
+    int max_nodes;
+    int64_t capacity;
+    int Hq, Hkv, window;
+    float scale;
+    void *workspace;                   // its first int32: status word
+    uint64_t timeout_ns, drain_ns;
+};
+size_t tree_attention_workspace();
+cudaError_t launch_tree_attention(const TreeAttnLaunch &L, cudaStream_t stream);
+
+struct TreeStepLaunch {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const int32_t *parents;
+    const float *state;
+    void *out;
+    const int32_t *cu_seqlens;
+    int num_seqs;
+    int64_t total_nodes;
+    int max_nodes, H, d, dtype;
+};
+cudaError_t launch_tree_step(const TreeStepLaunch &L, cudaStream_t stream);
+
+struct CacheWeightsLaunch {
+    const void *q;
+    const float *lse;
+    const void *k, *k_cache;
+    const float *w_in;
+    float *w_out, *w_new;
+    const int32_t *cu_queries, *cu_tokens, *cache_lens, *cache_pos, *seen;
+    int num_seqs;
+    int64_t total_queries, total_tokens, capacity;
+    int Hq, Hkv, window;
+    float scale;
+    void *workspace;                   // its first int32: status word
+    uint64_t timeout_ns, drain_ns;
+};
+size_t cache_weights_workspace();
+cudaError_t launch_cache_weights(const CacheWeightsLaunch &L, cudaStream_t stream);
+
+struct CacheInsertLaunch {
+    const void *k, *v;
+    void *k_cache, *v_cache;
+    const float *w_in;
+    float *w_out;
+    const int32_t *pos_in;
+    int32_t *pos_out;
+    const int32_t *lens_in;
+    int32_t *lens_out;
+    const int32_t *seen_in;
+    int32_t *seen_out;
+    const float *w_new;
+    int32_t *slots;
+    const int32_t *cu_seqlens;
+    int num_seqs;
+    int64_t total_tokens, capacity;
+    int Hkv, recent;
+    int64_t row_bytes;                 // of one key or value
+    void *workspace;
+};
+size_t cache_insert_workspace(int64_t total_tokens, int Hkv);
+cudaError_t launch_cache_insert(const CacheInsertLaunch &L, cudaStream_t stream);
+
 }  // namespace gdn

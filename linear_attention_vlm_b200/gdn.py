@@ -74,6 +74,20 @@ def _load():
     lib.gdn_rope.restype = i32
     lib.gdn_swa_attention.argtypes = [vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, f32, i32, vp, vp]
     lib.gdn_swa_attention.restype = i32
+    lib.gdn_tree_attention_workspace_size.argtypes = [i32, i64, i32, i64, i32, i32, i32, i32]
+    lib.gdn_tree_attention_workspace_size.restype = sz
+    lib.gdn_tree_attention.argtypes = [vp] * 10 + [vp, fp, i32, i64, i32, i64, i32, i32, i32, i32, f32, i32, vp, sz, vp]
+    lib.gdn_tree_attention.restype = i32
+    lib.gdn_tree_step.argtypes = [vp, vp, vp, fp, fp, vp, fp, vp, vp, i32, i64, i32, i32, i32, i32, i32, vp]
+    lib.gdn_tree_step.restype = i32
+    lib.gdn_cache_weights_workspace_size.argtypes = [i32, i64, i64, i64, i32, i32, i32, i32]
+    lib.gdn_cache_weights_workspace_size.restype = sz
+    lib.gdn_cache_weights.argtypes = [vp] * 12 + [i32, i64, i64, i64, i32, i32, i32, i32, f32, i32, vp, sz, vp]
+    lib.gdn_cache_weights.restype = i32
+    lib.gdn_cache_insert_workspace_size.argtypes = [i32, i64, i64, i32, i32, i32]
+    lib.gdn_cache_insert_workspace_size.restype = sz
+    lib.gdn_cache_insert.argtypes = [vp] * 15 + [i32, i64, i64, i32, i32, i32, i32, vp, sz, vp]
+    lib.gdn_cache_insert.restype = i32
     lib.gdn_session_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     lib.gdn_session_workspace_size.restype = sz
     lib.gdn_session_create.argtypes = [i32, i32, i32, i32, i32, i32, i32, f32, vp, vp]
@@ -494,6 +508,238 @@ def gdn_swa_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
     if st != GDN_OK:
         raise GdnError(st, "gdn_swa_attention")
     return out
+
+
+# ---------------------------------------------------------------- drafted trees and a bounded cache
+
+MAX_TREE_NODES = 64
+
+
+def _check(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev, optional: bool = False) -> None:
+    if t is None:
+        if optional:
+            return
+        raise ValueError("%s is missing" % what)
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise ValueError("%s must be %s %s on %s" % (what, dtype, list(shape), dev))
+
+
+def _check_cu(cu: Optional[torch.Tensor], B: int, dev, what: str = "cu_seqlens") -> None:
+    if cu is not None and (cu.dtype != torch.int32 or cu.device != dev or cu.shape != (B + 1,)):
+        raise ValueError("%s must be int32 [%d] on the same device" % (what, B + 1))
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev) -> Tuple[torch.Tensor, int]:
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev), need
+    if workspace.device != dev:
+        raise ValueError("workspace must be on %s" % dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _on_device(dev, fn, *args) -> int:
+    """fn(*args, current stream of dev), with dev current."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return fn(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(dev))
+
+
+def _tree_nodes(max_nodes: Optional[int], cu: Optional[torch.Tensor], T: int, B: int) -> int:
+    if max_nodes is not None:
+        return int(max_nodes)
+    return max(1, min(MAX_TREE_NODES, T)) if cu is not None else max(1, T // B)
+
+
+def gdn_tree_attention_workspace_size(num_seqs: int, total_nodes: int, max_nodes: int, capacity: int, Hq: int, Hkv: int,
+                                      d: int = 128, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(_load().gdn_tree_attention_workspace_size(num_seqs, total_nodes, max_nodes, capacity, Hq, Hkv, d,
+                                                         _dtype_code(dtype)))
+
+
+def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parents: Optional[torch.Tensor],
+                       k_cache: torch.Tensor, v_cache: torch.Tensor, cache_lens: torch.Tensor,
+                       cu_seqlens: Optional[torch.Tensor] = None, *, max_nodes: Optional[int] = None,
+                       cache_pos: Optional[torch.Tensor] = None, seen: Optional[torch.Tensor] = None, window: int = 0,
+                       scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of a tree of drafted tokens over a cache (include/gdn.h,
+    gdn_tree_attention).  q [T, Hq, 128], k, v [T, Hkv, 128] bf16, rotated;
+    parents [T] int32 (index in the sequence, -1 at a root) or None for chains;
+    k_cache, v_cache [B, capacity, Hkv, 128]; cache_lens [B] int32;
+    cu_seqlens int32 [B+1] or None (equal trees).  ``max_nodes`` bounds the
+    nodes of one sequence (default min(T, 64); a tighter bound costs less).
+    With cache_pos [B, Hkv, capacity] and seen [B] (int32) the window goes by
+    token positions.  Returns (o [T, Hq, 128], lse [T, Hq] fp32)."""
+    T, Hq, d = q.shape
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("gdn_tree_attention needs CUDA tensors")
+    B, cap, Hkv = k_cache.shape[:3]
+    dt = q.dtype
+    for name, t, shape in (("k", k, (T, Hkv, d)), ("v", v, (T, Hkv, d)), ("k_cache", k_cache, (B, cap, Hkv, d)),
+                           ("v_cache", v_cache, (B, cap, Hkv, d))):
+        _check(name, t, shape, dt, dev)
+    _check("parents", parents, (T,), torch.int32, dev, True)
+    _check("cache_lens", cache_lens, (B,), torch.int32, dev)
+    _check("cache_pos", cache_pos, (B, Hkv, cap), torch.int32, dev, True)
+    _check("seen", seen, (B,), torch.int32, dev, True)
+    _check_cu(cu_seqlens, B, dev)
+    n = _tree_nodes(max_nodes, cu_seqlens, T, B)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check("out", out, q.shape, dt, dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _check("lse", lse, (T, Hq), torch.float32, dev)
+    code = _dtype_code(dt)
+    lib = _load()
+    ws, ws_bytes = _scratch(workspace, lib.gdn_tree_attention_workspace_size(B, T, n, cap, Hq, Hkv, d, code), dev)
+    st = _on_device(dev, lib.gdn_tree_attention, _ptr(q), _ptr(k), _ptr(v), _ptr(parents), _ptr(cu_seqlens),
+                    _ptr(k_cache), _ptr(v_cache), _ptr(cache_lens), _ptr(cache_pos), _ptr(seen), _ptr(out), _ptr(lse),
+                    B, T, n, cap, Hq, Hkv, d, int(window), 0.0 if scale is None else float(scale), code, _ptr(ws),
+                    ws_bytes)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_tree_attention")
+    return out, lse
+
+
+def gdn_tree_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                  parents: Optional[torch.Tensor], state: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, *,
+                  max_nodes: Optional[int] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Read-out of every node of a tree of drafted tokens from one state per
+    sequence, which stays as it is (include/gdn.h, gdn_tree_step).  q, k, v
+    [T, H, d]; g, beta [T, H] fp32; parents [T] int32 or None for chains; state
+    [B, H, d, d] fp32; cu_seqlens int32 [B+1] or None (equal trees).  Returns
+    out [T, H, d]."""
+    T, H, d = q.shape
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("gdn_tree_step needs CUDA tensors")
+    B = state.shape[0]
+    _check("k", k, (T, H, d), q.dtype, dev)
+    _check("v", v, (T, H, d), q.dtype, dev)
+    _check("g", g, (T, H), torch.float32, dev)
+    _check("beta", beta, (T, H), torch.float32, dev)
+    _check("parents", parents, (T,), torch.int32, dev, True)
+    _check("state", state, (B, H, d, d), torch.float32, dev)
+    _check_cu(cu_seqlens, B, dev)
+    n = _tree_nodes(max_nodes, cu_seqlens, T, B)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _check("out", out, (T, H, d), q.dtype, dev)
+    st = _on_device(dev, _load().gdn_tree_step, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parents),
+                    _ptr(state), _ptr(out), _ptr(cu_seqlens), B, T, n, H, d, d, _dtype_code(q.dtype))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_tree_step")
+    return out
+
+
+def gdn_cache_weights_workspace_size(num_seqs: int, total_queries: int, total_tokens: int, capacity: int, Hq: int,
+                                     Hkv: int, d: int = 128, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(_load().gdn_cache_weights_workspace_size(num_seqs, total_queries, total_tokens, capacity, Hq, Hkv, d,
+                                                        _dtype_code(dtype)))
+
+
+def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cache: torch.Tensor, weights: torch.Tensor,
+                      cache_lens: torch.Tensor, cu_queries: Optional[torch.Tensor] = None,
+                      cu_tokens: Optional[torch.Tensor] = None, *, cache_pos: Optional[torch.Tensor] = None,
+                      seen: Optional[torch.Tensor] = None, window: int = 0, scale: Optional[float] = None,
+                      weights_out: Optional[torch.Tensor] = None, new_weights: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention weight per cache slot, added up (include/gdn.h,
+    gdn_cache_weights).  q [Tq, Hq, 128] bf16 and lse [Tq, Hq] fp32 of the last
+    queries of the new tokens, whose keys are k [T, Hkv, 128]; k_cache
+    [B, capacity, Hkv, 128]; weights [B, Hkv, capacity] fp32.  ``weights_out``
+    defaults to ``weights`` (in place).  Returns (weights_out, new_weights
+    [T, Hkv] fp32)."""
+    Tq, Hq, d = q.shape
+    T = k.shape[0]
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("gdn_cache_weights needs CUDA tensors")
+    B, cap, Hkv = k_cache.shape[:3]
+    dt = q.dtype
+    _check("lse", lse, (Tq, Hq), torch.float32, dev)
+    _check("k", k, (T, Hkv, d), dt, dev)
+    _check("k_cache", k_cache, (B, cap, Hkv, d), dt, dev)
+    _check("weights", weights, (B, Hkv, cap), torch.float32, dev)
+    _check("cache_lens", cache_lens, (B,), torch.int32, dev)
+    _check("cache_pos", cache_pos, (B, Hkv, cap), torch.int32, dev, True)
+    _check("seen", seen, (B,), torch.int32, dev, True)
+    _check_cu(cu_queries, B, dev, "cu_queries")
+    _check_cu(cu_tokens, B, dev, "cu_tokens")
+    if weights_out is None:
+        weights_out = weights
+    else:
+        _check("weights_out", weights_out, (B, Hkv, cap), torch.float32, dev)
+    if new_weights is None:
+        new_weights = torch.empty((T, Hkv), dtype=torch.float32, device=dev)
+    else:
+        _check("new_weights", new_weights, (T, Hkv), torch.float32, dev)
+    code = _dtype_code(dt)
+    lib = _load()
+    ws, ws_bytes = _scratch(workspace, lib.gdn_cache_weights_workspace_size(B, Tq, T, cap, Hq, Hkv, d, code), dev)
+    st = _on_device(dev, lib.gdn_cache_weights, _ptr(q), _ptr(lse), _ptr(k), _ptr(k_cache), _ptr(weights),
+                    _ptr(weights_out), _ptr(new_weights), _ptr(cu_queries), _ptr(cu_tokens), _ptr(cache_lens),
+                    _ptr(cache_pos), _ptr(seen), B, Tq, T, cap, Hq, Hkv, d, int(window),
+                    0.0 if scale is None else float(scale), code, _ptr(ws), ws_bytes)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_cache_weights")
+    return weights_out, new_weights
+
+
+def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     weights: torch.Tensor, cache_pos: torch.Tensor, cache_lens: torch.Tensor, seen: torch.Tensor,
+                     cu_seqlens: Optional[torch.Tensor] = None, *, recent: int = 0,
+                     new_weights: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+                     pos_out: Optional[torch.Tensor] = None, lens_out: Optional[torch.Tensor] = None,
+                     seen_out: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """New tokens enter a cache of constant size in place of its lightest slots
+    (include/gdn.h, gdn_cache_insert).  k, v [T, Hkv, d]; k_cache, v_cache
+    [B, capacity, Hkv, d], updated in place; weights fp32 and cache_pos int32
+    [B, Hkv, capacity]; cache_lens, seen int32 [B].  The ``*_out`` tensors
+    default to their inputs (in place).  Returns (weights_out, pos_out,
+    lens_out, seen_out, slots [T, Hkv] int32, -1 where a token did not stay)."""
+    T, Hkv, d = k.shape
+    dev = k.device
+    if dev.type != "cuda":
+        raise ValueError("gdn_cache_insert needs CUDA tensors")
+    B, cap = k_cache.shape[:2]
+    for name, t, shape in (("v", v, (T, Hkv, d)), ("k_cache", k_cache, (B, cap, Hkv, d)),
+                           ("v_cache", v_cache, (B, cap, Hkv, d))):
+        _check(name, t, shape, k.dtype, dev)
+    _check_cu(cu_seqlens, B, dev)
+    _check("new_weights", new_weights, (T, Hkv), torch.float32, dev, True)
+    _check("slots", slots, (T, Hkv), torch.int32, dev, True)
+    weights_out = weights if weights_out is None else weights_out
+    pos_out = cache_pos if pos_out is None else pos_out
+    lens_out = cache_lens if lens_out is None else lens_out
+    seen_out = seen if seen_out is None else seen_out
+    for name, t, shape, dt in (("weights", weights, (B, Hkv, cap), torch.float32),
+                               ("weights_out", weights_out, (B, Hkv, cap), torch.float32),
+                               ("cache_pos", cache_pos, (B, Hkv, cap), torch.int32),
+                               ("pos_out", pos_out, (B, Hkv, cap), torch.int32),
+                               ("cache_lens", cache_lens, (B,), torch.int32), ("lens_out", lens_out, (B,), torch.int32),
+                               ("seen", seen, (B,), torch.int32), ("seen_out", seen_out, (B,), torch.int32)):
+        _check(name, t, shape, dt, dev)
+    if slots is None:
+        slots = torch.empty((T, Hkv), dtype=torch.int32, device=dev)
+    code = _dtype_code(k.dtype)
+    lib = _load()
+    ws, ws_bytes = _scratch(workspace, lib.gdn_cache_insert_workspace_size(B, T, cap, Hkv, d, code), dev)
+    st = _on_device(dev, lib.gdn_cache_insert, _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(weights),
+                    _ptr(weights_out), _ptr(cache_pos), _ptr(pos_out), _ptr(cache_lens), _ptr(lens_out), _ptr(seen),
+                    _ptr(seen_out), _ptr(new_weights), _ptr(slots), _ptr(cu_seqlens), B, T, cap, Hkv, d, int(recent),
+                    code, _ptr(ws), ws_bytes)
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_cache_insert")
+    return weights_out, pos_out, lens_out, seen_out, slots
 
 
 class _SessionBuffers(ctypes.Structure):
