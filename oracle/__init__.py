@@ -135,3 +135,6 @@ from .layer_ops import (ACT_NONE, ACT_SILU, GATE_SIGMOID, GATE_SILU,  # noqa: E4
 # The hybrid block's other token mixer (plain numpy, fp64).
 from .attention import positions as rope_positions  # noqa: E402,F401
 from .attention import rope, swa_attention  # noqa: E402,F401
+
+# Drafted trees and the bounded cache (plain numpy, fp64).
+from . import decoding  # noqa: E402,F401
