@@ -487,7 +487,7 @@ size_t gdn_tree_attention_workspace_size(int num_seqs, int64_t total_nodes, int 
                                          int Hkv, int d, int dtype) {
     if (check_cache_attention(num_seqs, total_nodes, 0, capacity, Hq, Hkv, d, 0, 0.f, dtype) != GDN_OK) return 0;
     if (max_nodes < 1 || max_nodes > GDN_MAX_TREE_NODES) return 0;
-    return gdn::tree_attention_workspace();
+    return gdn::tree_attention_workspace(num_seqs, max_nodes, Hq, Hkv);
 }
 
 int gdn_tree_attention(const void *q, const void *k, const void *v, const int32_t *parents,
@@ -526,9 +526,7 @@ int gdn_tree_attention(const void *q, const void *k, const void *v, const int32_
     L.workspace = workspace;
     L.timeout_ns = g_wait_limit_ns;
     L.drain_ns = kWaitLimitNs;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), s);
-    if (e == cudaSuccess) e = gdn::launch_tree_attention(L, s);
+    const cudaError_t e = gdn::launch_tree_attention(L, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GDN_OK : cuda_fail(e);
 }
 

@@ -144,7 +144,7 @@ struct TreeAttnLaunch {
     void *workspace;                   // its first int32: status word
     uint64_t timeout_ns, drain_ns;
 };
-size_t tree_attention_workspace();
+size_t tree_attention_workspace(int num_seqs, int max_nodes, int Hq, int Hkv);
 cudaError_t launch_tree_attention(const TreeAttnLaunch &L, cudaStream_t stream);
 
 struct TreeStepLaunch {
