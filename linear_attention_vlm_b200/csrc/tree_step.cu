@@ -3,12 +3,27 @@
 //
 // With anc(i) the node and its ancestors, G_i = sum of g over anc(i) and S the
 // state before the tree, unrolling the recurrence along a path gives
-//   S_i = exp(G_i) S + sum_{j in anc(i)} exp(G_i - G_j) u_j k_j^T
-//   u_i = beta_i (v_i - exp(G_i) S k_i - sum_{j in anc(i), j != i} exp(G_i - G_j) (k_j . k_i) u_j)
-//   o_i = exp(G_i) S q_i + sum_{j in anc(i)} exp(G_i - G_j) (k_j . q_i) u_j
+//   S_i = e^G_i S + sum_{j in anc(i)} e^(G_i - G_j) u_j k_j^T
+//   (I + A) U = R,   R_i = beta_i (v_i - e^G_i S k_i),   A_ij = beta_i e^(G_i - G_j) k_i . k_j  (j a proper ancestor)
+//   o_i = e^G_i S q_i + sum_j M_ij R_j,   M = P (I + A)^-1,   P_ij = e^(G_i - G_j) q_i . k_j  (j in anc(i))
 // The exponents are sums of g over part of a path, so no factor exceeds 1.
-// The products with S do not depend on the tree; u_i is solved node by node,
-// every value channel (row of S) on its own.
+// Only S k and S q touch the state, and M needs no state at all: it is found by
+// back substitution, a thread per row, while the tensor cores form S k and S q.
+//
+// What bounds it: the state, 4 d^2 bytes per head, read once; then the products
+// (2 + 2 splits) n d^2.  One CTA per (sequence, head).  A warp owns 16 rows of S
+// (value channels), which go from memory straight into the A fragments of
+// mma.sync: lane quads read 64 consecutive bytes of a row, and the keys and
+// queries are read in the same order of channels, so no shuffle or shared
+// memory is needed for S.  The result fragments (value channel x node) are the
+// A fragments of the second product, with M: nothing of size n x d leaves the
+// registers between them.  tcgen05 would want S as bf16 pairs in shared memory
+// and twice the passes through it for products this small (n <= 64 columns).
+//
+// Precision: with bf16 inputs S, R and M enter as hi + lo bf16 pairs (2^-17
+// relative, far below the rounding of the output); with fp32 inputs every
+// operand is split into two tf32 numbers and three products are taken (2^-21).
+// All sums are fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -18,91 +33,393 @@
 namespace gdn {
 namespace {
 
-// One CTA per (sequence, head), a thread per value channel.
-template <typename T, int D>
-__global__ void __launch_bounds__(D) tree_step_kernel(const TreeStepLaunch L, int64_t uniform_len) {
-    extern __shared__ float sm[];
-    float *ks = sm;                        // [64][D]
-    float *qs = ks + kMaxNodes * D;        // [64][D]
-    float *us = qs + kMaxNodes * D;        // [64][D], a thread's own column
-    float *kk = us + kMaxNodes * D;        // [64][64] exp(G_i - G_j) k_j . k_i, 0 where j is no ancestor
-    float *qk = kk + kMaxNodes * kMaxNodes;
-    __shared__ float Gs[kMaxNodes];
-    __shared__ unsigned long long anc[kMaxNodes];
-    const int tid = threadIdx.x, b = blockIdx.x / L.H, h = blockIdx.x % L.H;
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float4 load_stream(const float *p) {   // read once: keep it out of L1
+    float4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// hi + lo = (x, y) up to 2^-17, two bf16 each
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(x, y);
+    lo = pack2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+
+// hi + lo = x up to 2^-21: 11 significant bits each, cut and then rounded by the unit
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+// The product fragments of 16 channels.  An A fragment holds two rows (lane
+// group g = lane / 4: rows g and g + 8), a B fragment one (row g); of a row, lane
+// t = lane % 4 has channels 4 t .. 4 t + 3.  Both sides use the same order, so
+// the sum over channels is the same.
+template <typename T> struct Frag;
+
+template <> struct Frag<__nv_bfloat16> {
+    struct A { uint32_t hi[4], lo[4]; };
+    struct B { uint32_t b[2]; };
+    static constexpr int kPad = 16;     // elements behind a row of keys: conflict-free 8-byte reads
+    __device__ static float exp(float x) { return __expf(x); }
+    __device__ static void split(const float4 &u, const float4 &w, A &a) {
+        split_bf16(u.x, u.y, a.hi[0], a.lo[0]);
+        split_bf16(w.x, w.y, a.hi[1], a.lo[1]);
+        split_bf16(u.z, u.w, a.hi[2], a.lo[2]);
+        split_bf16(w.z, w.w, a.hi[3], a.lo[3]);
+    }
+    __device__ static void load_b(const __nv_bfloat16 *row, B &b) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(row);
+        b.b[0] = v.x;
+        b.b[1] = v.y;
+    }
+    __device__ static void mma(float (&c)[4], const A &a, const B &b) {
+        mma_bf16(c, a.hi, b.b[0], b.b[1]);
+        mma_bf16(c, a.lo, b.b[0], b.b[1]);
+    }
+    // keys and queries as A rows: exact in bf16
+    __device__ static void mma_rows(float (&c)[4], const __nv_bfloat16 *r0, const __nv_bfloat16 *r1, const B &b) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(r0), w = *reinterpret_cast<const uint2 *>(r1);
+        const uint32_t a[4] = {u.x, w.x, u.y, w.y};
+        mma_bf16(c, a, b.b[0], b.b[1]);
+    }
+    // R (two accumulator fragments, 16 nodes) times M (row of node i: m at nodes 2t, 2t + 1 of each fragment)
+    __device__ static void mma_nodes(float (&c)[4], const float (&x)[4], const float (&y)[4], const float2 &m0, const float2 &m1) {
+        uint32_t hi[4], lo[4], mh[2], ml[2];
+        split_bf16(x[0], x[1], hi[0], lo[0]);
+        split_bf16(x[2], x[3], hi[1], lo[1]);
+        split_bf16(y[0], y[1], hi[2], lo[2]);
+        split_bf16(y[2], y[3], hi[3], lo[3]);
+        split_bf16(m0.x, m0.y, mh[0], ml[0]);
+        split_bf16(m1.x, m1.y, mh[1], ml[1]);
+        mma_bf16(c, lo, mh[0], mh[1]);
+        mma_bf16(c, hi, ml[0], ml[1]);
+        mma_bf16(c, hi, mh[0], mh[1]);
+    }
+};
+
+template <> struct Frag<float> {
+    struct A { uint32_t hi[2][4], lo[2][4]; };
+    struct B { uint32_t hi[4], lo[4]; };
+    static constexpr int kPad = 16;     // conflict-free 16-byte reads
+    __device__ static float exp(float x) { return expf(x); }
+    __device__ static void split(const float4 &u, const float4 &w, A &a) {
+        split_tf32(u.x, a.hi[0][0], a.lo[0][0]);
+        split_tf32(w.x, a.hi[0][1], a.lo[0][1]);
+        split_tf32(u.y, a.hi[0][2], a.lo[0][2]);
+        split_tf32(w.y, a.hi[0][3], a.lo[0][3]);
+        split_tf32(u.z, a.hi[1][0], a.lo[1][0]);
+        split_tf32(w.z, a.hi[1][1], a.lo[1][1]);
+        split_tf32(u.w, a.hi[1][2], a.lo[1][2]);
+        split_tf32(w.w, a.hi[1][3], a.lo[1][3]);
+    }
+    __device__ static void load_b(const float *row, B &b) {
+        const float4 v = *reinterpret_cast<const float4 *>(row);
+        split_tf32(v.x, b.hi[0], b.lo[0]);
+        split_tf32(v.y, b.hi[1], b.lo[1]);
+        split_tf32(v.z, b.hi[2], b.lo[2]);
+        split_tf32(v.w, b.hi[3], b.lo[3]);
+    }
+    __device__ static void mma(float (&c)[4], const A &a, const B &b) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            mma_tf32(c, a.lo[s], b.hi[2 * s], b.hi[2 * s + 1]);
+            mma_tf32(c, a.hi[s], b.lo[2 * s], b.lo[2 * s + 1]);
+            mma_tf32(c, a.hi[s], b.hi[2 * s], b.hi[2 * s + 1]);
+        }
+    }
+    __device__ static void mma_rows(float (&c)[4], const float *r0, const float *r1, const B &b) {
+        A a;
+        split(*reinterpret_cast<const float4 *>(r0), *reinterpret_cast<const float4 *>(r1), a);
+        mma(c, a, b);
+    }
+    __device__ static void mma_nodes(float (&c)[4], const float (&x)[4], const float (&y)[4], const float2 &m0, const float2 &m1) {
+        const float *src[2] = {x, y};
+        const float2 ms[2] = {m0, m1};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t hi[4], lo[4], mh[2], ml[2];   // nodes 2t, 2t + 1 as the k indices t, t + 4
+            split_tf32(src[s][0], hi[0], lo[0]);
+            split_tf32(src[s][2], hi[1], lo[1]);
+            split_tf32(src[s][1], hi[2], lo[2]);
+            split_tf32(src[s][3], hi[3], lo[3]);
+            split_tf32(ms[s].x, mh[0], ml[0]);
+            split_tf32(ms[s].y, mh[1], ml[1]);
+            mma_tf32(c, lo, mh[0], mh[1]);
+            mma_tf32(c, hi, ml[0], ml[1]);
+            mma_tf32(c, hi, mh[0], mh[1]);
+        }
+    }
+};
+
+// Shared memory of a CTA for up to NP nodes.
+template <typename T, int D, int NP> struct Shape {
+    static constexpr int kMain = D / 16;                       // warps with rows of S
+    static constexpr int kSolve = NP >= 64 ? 2 : 1;            // warps with rows of M
+    static constexpr int kThreads = 32 * (kMain + kSolve);
+    static constexpr int kRow = D + Frag<T>::kPad;             // elements of a key or query row
+    static constexpr int kVRow = D + (sizeof(T) == 2 ? 8 : 4); // of a value row, later the output
+    static constexpr int kA = NP, kP = NP + 8;                 // floats of a row of A and of P (then M)
+    static constexpr size_t kv = 2 * NP * kRow * sizeof(T), ka = kv + NP * kVRow * sizeof(T), kp = ka + NP * kA * 4,
+                            kn = kp + NP * kP * 4, kBytes = kn + NP * (4 + 4 + 8 + 4);
+};
+
+template <typename T, int D, int NP>
+__global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, NP <= 16 ? 2 : 1)
+    tree_step_kernel(const TreeStepLaunch L, int64_t uniform_len) {
+    using S = Shape<T, D, NP>;
+    using F = Frag<T>;
+    extern __shared__ __align__(16) uint8_t sm[];
+    T *kq = reinterpret_cast<T *>(sm);                        // [2 NP][kRow]: keys, then queries
+    T *vo = reinterpret_cast<T *>(sm + S::kv);                // [NP][kVRow]
+    float *as = reinterpret_cast<float *>(sm + S::ka);        // [NP][kA]
+    float *ps = reinterpret_cast<float *>(sm + S::kp);        // [NP][kP]
+    unsigned long long *anc = reinterpret_cast<unsigned long long *>(sm + S::kn);   // [NP]
+    float *Gs = reinterpret_cast<float *>(anc + NP), *bs = Gs + NP;                 // [NP]
+    int *up = reinterpret_cast<int *>(bs + NP);                                      // [NP]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int b = blockIdx.x / L.H, h = blockIdx.x % L.H;
     int64_t bos;
-    const int n = seq_rows(L.cu_seqlens, uniform_len, L.total_nodes, b, L.max_nodes, bos);
-    const T *q = static_cast<const T *>(L.q), *k = static_cast<const T *>(L.k), *v = static_cast<const T *>(L.v);
-    for (int i = 0; i < n; ++i) {
-        const int64_t at = ((bos + i) * L.H + h) * D + tid;
-        ks[i * D + tid] = to_f32(k[at]);
-        qs[i * D + tid] = to_f32(q[at]);
+    const int n = seq_rows(L.cu_seqlens, uniform_len, L.total_nodes, b, min(L.max_nodes, NP), bos);
+    if (n == 0) return;
+    const bool main_warp = warp < S::kMain;
+
+    // this warp's 16 rows of S, in flight while the tree is prepared
+    constexpr int KS = D / 16;
+    float4 s0[KS], s1[KS];
+    if (main_warp) {
+        const float *row = L.state + ((int64_t)blockIdx.x * D + 16 * warp + g) * D + 4 * t;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            s0[s] = L.state ? load_stream(row + 16 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
+            s1[s] = L.state ? load_stream(row + 8 * D + 16 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
-    if (tid < n) {
-        unsigned long long a = 0;
+    // keys, queries and values; rows behind the last node are zero
+    {
+        constexpr int V = 16 / sizeof(T), per = D / V;
+        for (int e = tid; e < 3 * NP * per; e += S::kThreads) {
+            const int m = e / (NP * per), i = e / per % NP, c = e % per * V;
+            const T *src = static_cast<const T *>(m == 0 ? L.k : m == 1 ? L.q : L.v) + ((bos + i) * L.H + h) * D + c;
+            const uint4 x = i < n ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(m < 2 ? kq + (m * NP + i) * S::kRow + c : vo + i * S::kVRow + c) = x;
+        }
+    }
+    if (!main_warp) {
+        // ancestors and path sums by doubling: every round a node takes over
+        // what its current ancestor pointer has gathered
+        const int i = tid - 32 * S::kMain;
         float G = 0.f;
-        for (int p = tid; p >= 0; p = tree_parent(L.parents, bos, p)) {
-            a |= 1ull << p;
-            G += L.g[(bos + p) * L.H + h];
+        unsigned long long a = 0;
+        int p = -1;
+        if (i < NP) {
+            if (i < n) {
+                p = tree_parent(L.parents, bos, i);
+                G = L.g[(bos + i) * L.H + h];
+                bs[i] = L.beta[(bos + i) * L.H + h];
+                a = 1ull << i;
+            } else {
+                bs[i] = 0.f;
+            }
         }
-        anc[tid] = a;
-        Gs[tid] = G;
+#pragma unroll 1
+        for (int round = 1; round < NP; round *= 2) {
+            if (i < NP) {
+                Gs[i] = G;
+                anc[i] = a;
+                up[i] = p;
+            }
+            asm volatile("bar.sync 1, %0;" ::"r"(32 * S::kSolve) : "memory");
+            if (p >= 0) {
+                G += Gs[p];
+                a |= anc[p];
+                p = up[p];
+            }
+            asm volatile("bar.sync 1, %0;" ::"r"(32 * S::kSolve) : "memory");
+        }
+        if (i < NP) {
+            Gs[i] = G;
+            anc[i] = a;
+        }
     }
     __syncthreads();
-    for (int e = tid; e < n * n; e += D) {
-        const int i = e / n, j = e % n;
-        float a = 0.f, c = 0.f;
-        if (anc[i] >> j & 1) {
-            for (int x = 0; x < D; ++x) {
-                a = fmaf(ks[j * D + x], ks[i * D + x], a);
-                c = fmaf(ks[j * D + x], qs[i * D + x], c);
+
+    // A and P: products of keys and queries with keys, decayed, 0 where j is no ancestor
+    const int tiles = (n + 7) / 8;   // 8 nodes each
+    if (main_warp) {
+#pragma unroll 1
+        for (int mt = warp; mt < 2 * NP / 16; mt += S::kMain) {
+            const bool reads = mt >= NP / 16;                       // a tile of queries
+            const int i0 = (mt % (NP / 16)) * 16;
+            if (i0 >= n) continue;
+            const T *r0 = kq + (mt * 16 + g) * S::kRow + 4 * t, *r1 = r0 + 8 * S::kRow;
+            const int i[2] = {i0 + g, i0 + g + 8};
+            const unsigned long long an[2] = {anc[i[0]], anc[i[1]]};
+            const float G[2] = {Gs[i[0]], Gs[i[1]]}, be[2] = {bs[i[0]], bs[i[1]]};
+#pragma unroll 1
+            for (int j0 = 0; j0 < NP; j0 += 8) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                if (j0 < i0 + 16) {                                // ancestors come before
+                    const T *rb = kq + (j0 + g) * S::kRow + 4 * t;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        typename F::B fb;
+                        F::load_b(rb + 16 * s, fb);
+                        F::mma_rows(c, r0 + 16 * s, r1 + 16 * s, fb);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = j0 + 2 * t + (e & 1), r = e >> 1;
+                    const bool see = (an[r] >> j & 1) && (reads || j != i[r]);
+                    const float v = see ? c[e] * F::exp(G[r] - Gs[j]) : 0.f;
+                    if (reads) ps[i[r] * S::kP + j] = v;
+                    else as[i[r] * S::kA + j] = v * be[r];
+                }
             }
-            const float f = expf(Gs[i] - Gs[j]);
-            a *= f;
-            c *= f;
         }
-        kk[i * kMaxNodes + j] = a;
-        qk[i * kMaxNodes + j] = c;
     }
     __syncthreads();
-    const float *srow = L.state ? L.state + ((int64_t)blockIdx.x * D + tid) * D : nullptr;
-    for (int i = 0; i < n; ++i) {
-        float sk = 0.f, sq = 0.f;
-        if (srow)
-            for (int x = 0; x < D; ++x) {
-                const float s = srow[x];
-                sk = fmaf(s, ks[i * D + x], sk);
-                sq = fmaf(s, qs[i * D + x], sq);
+
+    if (!main_warp) {
+        // M = P (I + A)^-1, row i: m_l = p_l - sum over l' > l of m_l' A_l'l
+        const int i = tid - 32 * S::kMain;
+        if (i < NP) {
+            float m[NP];
+            float *row = ps + i * S::kP;
+#pragma unroll
+            for (int j = 0; j < NP; j += 4) {
+                const float4 v = i < n ? *reinterpret_cast<const float4 *>(row + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                m[j] = v.x;
+                m[j + 1] = v.y;
+                m[j + 2] = v.z;
+                m[j + 3] = v.w;
             }
-        const float gamma = expf(Gs[i]);
-        const int64_t at = (bos + i) * L.H + h;
-        float u = to_f32(v[at * D + tid]) - gamma * sk, o = gamma * sq;
-        for (int j = 0; j < i; ++j) {
-            u = fmaf(-kk[i * kMaxNodes + j], us[j * D + tid], u);
-            o = fmaf(qk[i * kMaxNodes + j], us[j * D + tid], o);
+#pragma unroll
+            for (int l = NP - 1; l > 0; --l) {
+                if (l < n) {
+#pragma unroll
+                    for (int j = 0; j < l; j += 4) {
+                        const float4 a = *reinterpret_cast<const float4 *>(as + l * S::kA + j);
+                        m[j] = fmaf(-m[l], a.x, m[j]);
+                        if (j + 1 < l) m[j + 1] = fmaf(-m[l], a.y, m[j + 1]);
+                        if (j + 2 < l) m[j + 2] = fmaf(-m[l], a.z, m[j + 2]);
+                        if (j + 3 < l) m[j + 3] = fmaf(-m[l], a.w, m[j + 3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NP; j += 4) *reinterpret_cast<float4 *>(row + j) = make_float4(m[j], m[j + 1], m[j + 2], m[j + 3]);
         }
-        u *= L.beta[at];
-        us[i * D + tid] = u;
-        o = fmaf(qk[i * kMaxNodes + i], u, o);
-        static_cast<T *>(L.out)[at * D + tid] = from_f32<T>(o);
+        __syncthreads();
+        return;
+    }
+
+    // S k and S q: value channels g, g + 8 of the warp's 16 by nodes 2t, 2t + 1 of each 8
+    float xk[NP / 8][4], xq[NP / 8][4];
+#pragma unroll
+    for (int j = 0; j < NP / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xk[j][e] = xq[j][e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        typename F::A a;
+        F::split(s0[s], s1[s], a);
+#pragma unroll
+        for (int j = 0; j < NP / 8; ++j) {
+            if (j < tiles) {
+                typename F::B fk, fq;
+                F::load_b(kq + (8 * j + g) * S::kRow + 16 * s + 4 * t, fk);
+                F::load_b(kq + (NP + 8 * j + g) * S::kRow + 16 * s + 4 * t, fq);
+                F::mma(xk[j], a, fk);
+                F::mma(xq[j], a, fq);
+            }
+        }
+    }
+    // R in place of S k, the first term of the output in place of S q
+#pragma unroll
+    for (int j = 0; j < NP / 8; ++j) {
+        if (j < tiles) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 8 * j + 2 * t + (e & 1), c = 16 * warp + g + 8 * (e >> 1);
+                const float gamma = F::exp(Gs[i]);
+                xk[j][e] = bs[i] * (to_f32(vo[i * S::kVRow + c]) - gamma * xk[j][e]);
+                xq[j][e] *= gamma;
+            }
+        }
+    }
+    __syncthreads();   // M is there
+#pragma unroll
+    for (int i = 0; i < NP / 8; ++i) {
+        if (i < tiles) {
+#pragma unroll
+            for (int k = 0; k <= i / 2; ++k) {   // 16 nodes: none after node tile i is an ancestor
+                const float *m = ps + (8 * i + g) * S::kP + 16 * k + 2 * t;
+                F::mma_nodes(xq[i], xk[2 * k], xk[2 * k + 1], *reinterpret_cast<const float2 *>(m), *reinterpret_cast<const float2 *>(m + 8));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)          // over the value that this thread alone has read
+                vo[(8 * i + 2 * t + (e & 1)) * S::kVRow + 16 * warp + g + 8 * (e >> 1)] = from_f32<T>(xq[i][e]);
+        }
+    }
+    __syncwarp();
+    // the warp's 16 channels of every node
+    constexpr int V = 16 / sizeof(T), per = 16 / V;
+    for (int e = lane; e < n * per; e += 32) {
+        const int i = e / per, c = 16 * warp + e % per * V;
+        *reinterpret_cast<uint4 *>(static_cast<T *>(L.out) + ((bos + i) * L.H + h) * D + c) =
+            *reinterpret_cast<const uint4 *>(vo + i * S::kVRow + c);
     }
 }
 
-template <typename T, int D>
-cudaError_t launch(const TreeStepLaunch &L, cudaStream_t stream) {
-    const int64_t uniform_len = L.cu_seqlens ? 0 : L.total_nodes / L.num_seqs;
-    const int smem = (3 * kMaxNodes * D + 2 * kMaxNodes * kMaxNodes) * 4;
-    cudaError_t e = cudaFuncSetAttribute(tree_step_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename T, int D, int NP> cudaError_t launch(const TreeStepLaunch &L, cudaStream_t stream) {
+    using S = Shape<T, D, NP>;
+    static bool done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    tree_step_kernel<T, D><<<L.num_seqs * L.H, D, smem, stream>>>(L, uniform_len);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev]) {
+        e = cudaFuncSetAttribute(tree_step_kernel<T, D, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    const int64_t uniform_len = L.cu_seqlens ? 0 : L.total_nodes / L.num_seqs;
+    tree_step_kernel<T, D, NP><<<L.num_seqs * L.H, S::kThreads, S::kBytes, stream>>>(L, uniform_len);
     return cudaGetLastError();
+}
+
+// The node count fixes the registers that hold S k, S q and a row of M, so it
+// is a compile-time bound: 16, 32 or 64.
+template <typename T, int D> cudaError_t launch_nodes(const TreeStepLaunch &L, cudaStream_t stream) {
+    if (L.max_nodes <= 16) return launch<T, D, 16>(L, stream);
+    if (L.max_nodes <= 32) return launch<T, D, 32>(L, stream);
+    return launch<T, D, 64>(L, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_step(const TreeStepLaunch &L, cudaStream_t stream) {
-    if (L.dtype == GDN_F32) return L.d == 128 ? launch<float, 128>(L, stream) : launch<float, 64>(L, stream);
-    return L.d == 128 ? launch<__nv_bfloat16, 128>(L, stream) : launch<__nv_bfloat16, 64>(L, stream);
+    if (L.dtype == GDN_F32) return L.d == 128 ? launch_nodes<float, 128>(L, stream) : launch_nodes<float, 64>(L, stream);
+    return L.d == 128 ? launch_nodes<__nv_bfloat16, 128>(L, stream) : launch_nodes<__nv_bfloat16, 64>(L, stream);
 }
 
 }  // namespace gdn
