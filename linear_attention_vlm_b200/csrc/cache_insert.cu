@@ -5,22 +5,33 @@
 // bits of the weight made monotone, all ones for a recent position, zero for
 // NaN.  E = candidates - capacity of them give way: those below the E-th
 // smallest key tau and, of the ones equal to it, the latest.  tau is found
-// digit by digit (8 bits, a histogram in shared memory each).  Evicted slots and
-// empty ones, ascending, take the new tokens that stay, ascending: slots that
-// stay do not move, so the rows copied are the new tokens' alone, and no copy
-// reads what another writes.
+// digit by digit (11, 11 and 10 bits), a histogram in shared memory each.
+// Evicted slots and empty ones, ascending, take the new tokens that stay, ascending:
+// slots that stay do not move, so the rows copied are the new tokens' alone,
+// and no copy reads what another writes.
 //
-// Two kernels: the selection, one CTA per (sequence, head), which also writes
-// weights and positions; then the copy of keys and values, one warp per row.
+// Two kernels: the selection, which also writes weights and positions, then
+// the copy of keys and values, one warp per row.  Weights and positions are 8
+// bytes a slot and are read once: the keys stay in registers, kKeep a thread.
+// What bounds the selection is the chain of histograms (latency, a
+// few microseconds), so a (sequence, head) with more candidates than one CTA
+// keeps is spread over a cluster of CTAs that read one another's histograms.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include "sm100.cuh"
 #include "tree.cuh"
 
 namespace gdn {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kKeep = 10;          // keys a thread holds: 10240 candidates a CTA; the rest are read again
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;     // the portable limit
 constexpr unsigned kAll = 0xffffffffu;
 
 // order-preserving bits of a weight; NaN below everything, -0 as 0
@@ -30,31 +41,36 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// Exclusive prefix over the CTA's warps of a per-warp count; every thread of
-// a warp gets its warp's prefix, `total` the sum.
-__device__ __forceinline__ int warp_prefix(int count, int *sh, int &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    __syncthreads();
-    if (lane == 0) sh[warp] = count;
-    __syncthreads();
-    int v = sh[lane];
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += t;
-    }
-    total = __shfl_sync(kAll, incl, 31);
-    return __shfl_sync(kAll, incl - v, warp);
+// One more in hist[digit] for every lane with `in`.  Weights are often alike
+// (zeros above all): the lanes that share the first lane's digit add once.
+__device__ __forceinline__ void count_digit(unsigned *hist, bool in, uint32_t digit) {
+    const unsigned act = __ballot_sync(kAll, in);
+    if (!act) return;
+    const int first = __ffs(act) - 1;
+    const uint32_t lead = __shfl_sync(kAll, digit, first);
+    const unsigned same = __ballot_sync(kAll, in && digit == lead);
+    if ((int)(threadIdx.x & 31) == first) atomicAdd(&hist[lead], __popc(same));
+    else if (in && digit != lead) atomicAdd(&hist[digit], 1u);
 }
 
+struct Counts {
+    int below_slot, below_new, equal_slot, equal_new;   // keys below tau and equal to it, among slots and new tokens
+};
+
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheInsertLaunch L, int64_t uniform_len) {
-    __shared__ unsigned hist[256];
-    __shared__ int scan_sh[kSelWarps];
-    __shared__ unsigned prefix_sh;
-    __shared__ int rest_sh;
+    __shared__ unsigned hist[3][kBins];
+    __shared__ int scan_sh[4][kSelWarps];
+    __shared__ Counts tot_sh;
+    __shared__ int found_sh[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / L.Hkv, h = blockIdx.x % L.Hkv;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    auto sync_all = [&] {
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+    };
+    const int bh = blockIdx.x / ctas, b = bh / L.Hkv, h = bh % L.Hkv;
+    sm100::grid_dep_launch();
     int64_t t0;
     const int m = seq_rows(L.cu_seqlens, uniform_len, L.total_tokens, b, INT32_MAX, t0);
     const int cap = (int)L.capacity;
@@ -64,89 +80,161 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
     const int64_t base = ((int64_t)b * L.Hkv + h) * cap;
     auto new_weight = [&](int j) { return L.w_new ? L.w_new[(t0 + j) * L.Hkv + h] : 0.f; };
     auto key_of = [&](int i) -> uint32_t {
-        if (i < len) return seen + m - L.pos_in[base + i] <= L.recent ? 0xffffffffu : weight_key(L.w_in[base + i]);
+        if (i < len) {
+            const int pos = L.pos_in[base + i];
+            const float w = L.w_in[base + i];
+            return seen + m - pos <= L.recent ? 0xffffffffu : weight_key(w);
+        }
         return C - i <= L.recent ? 0xffffffffu : weight_key(new_weight(i - len));
+    };
+    // a warp owns `rounds` x 32 consecutive candidates from c0 on, so ranks are running counts
+    const int rounds = (int)(((int64_t)C + ctas * kSelThreads - 1) / (ctas * kSelThreads));
+    const int64_t c0_ = ((int64_t)rank * kSelWarps + warp) * rounds * 32;
+    const int c0 = (int)min((int64_t)C, c0_);
+    uint32_t kept[kKeep];
+    if (evict > 0) {
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k) {
+            const int i = c0 + 32 * k + lane;
+            kept[k] = k < rounds && i < C ? key_of(i) : 0u;
+        }
+    }
+    // calls f(candidate, it exists, key) for the warp's candidates, all lanes together
+    auto walk = [&](auto f) {
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k)
+            if (k < rounds) f(c0 + 32 * k + lane, c0 + 32 * k + lane < C, kept[k]);
+        for (int k = kKeep; k < rounds; ++k) {
+            const int i = c0 + 32 * k + lane;
+            f(i, i < C, evict > 0 && i < C ? key_of(i) : 0u);
+        }
     };
 
     // tau, and how many of the candidates equal to it give way
     uint32_t tau = 0;
     int ties = 0;
     if (evict > 0) {
+        for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+        __syncthreads();
         int rest = evict;
-        for (int shift = 24; shift >= 0; shift -= 8) {
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            walk([&](int, bool in, uint32_t key) {
+                const bool on = in && (pass == 0 || key >> (shift + bits) == tau >> (shift + bits));
+                count_digit(hist[pass], on, (key >> shift) & (kBins - 1) & ((1u << bits) - 1));
+            });
+            sync_all();
+            // bins 2 tid, 2 tid + 1 of all CTAs, and what lies before them
+            unsigned n0 = 0, n1 = 0;
+            for (int c = 0; c < ctas; ++c) {
+                const unsigned *other = ctas > 1 ? cluster.map_shared_rank(&hist[pass][0], c) : hist[pass];
+                const uint2 v = *reinterpret_cast<const uint2 *>(other + 2 * tid);
+                n0 += v.x;
+                n1 += v.y;
+            }
+            int incl = (int)(n0 + n1);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(kAll, incl, o);
+                if (lane >= o) incl += t;
+            }
+            if (lane == 31) scan_sh[0][warp] = incl;
             __syncthreads();
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < C; i += kSelThreads) {
-                const uint32_t key = key_of(i);
-                if (shift == 24 || (key >> (shift + 8)) == (tau >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1u);
+            int add = lane < warp ? scan_sh[0][lane] : 0;
+            add = __reduce_add_sync(kAll, add);
+            const int before = add + incl - (int)(n0 + n1);
+            if (before < rest && rest <= before + (int)(n0 + n1)) {
+                const bool second = rest > before + (int)n0;
+                found_sh[0] = 2 * tid + second;
+                found_sh[1] = rest - before - (second ? (int)n0 : 0);
             }
             __syncthreads();
-            if (tid == 0) {
-                int r = rest, d = 0;
-                while (d < 255 && (int)hist[d] < r) r -= hist[d++];
-                prefix_sh = d;
-                rest_sh = r;
-            }
-            __syncthreads();
-            tau |= prefix_sh << shift;
-            rest = rest_sh;
+            tau |= (uint32_t)found_sh[0] << shift;
+            rest = found_sh[1];
         }
         ties = rest;
     }
 
-    // a warp owns consecutive candidates, so ranks are running counts
-    const int span = ((C + kSelThreads - 1) / kSelThreads) * 32, c0 = warp * span, c1 = min(C, c0 + span);
-    int n_eq = 0, all_eq = 0;
+    // counts before this warp, over the cluster
+    Counts mine = {0, 0, 0, 0};
     if (evict > 0)
-        for (int i = c0 + lane; i - lane < c1; i += 32) n_eq += __popc(__ballot_sync(kAll, i < c1 && key_of(i) == tau));
-    const int eq0 = warp_prefix(n_eq, scan_sh, all_eq);
-    const unsigned below = (1u << lane) - 1;
-    // calls f(candidate, gives way) for the warp's candidates, all lanes together
-    auto walk = [&](auto f) {
-        int eq = eq0;
-        for (int i = c0 + lane; i - lane < c1; i += 32) {
-            const bool in = i < c1;
-            const uint32_t key = in && evict > 0 ? key_of(i) : 0xffffffffu;
-            const unsigned same = __ballot_sync(kAll, in && evict > 0 && key == tau);
-            const bool gone = in && evict > 0 && (key < tau || (key == tau && eq + __popc(same & below) >= all_eq - ties));
-            eq += __popc(same);
-            f(i, in, gone);
+        walk([&](int i, bool in, uint32_t key) {
+            const bool slot = i < len;
+            mine.below_slot += __popc(__ballot_sync(kAll, in && slot && key < tau));
+            mine.below_new += __popc(__ballot_sync(kAll, in && !slot && key < tau));
+            mine.equal_slot += __popc(__ballot_sync(kAll, in && slot && key == tau));
+            mine.equal_new += __popc(__ballot_sync(kAll, in && !slot && key == tau));
+        });
+    __syncthreads();
+    if (lane == 0) {
+        scan_sh[0][warp] = mine.below_slot;
+        scan_sh[1][warp] = mine.below_new;
+        scan_sh[2][warp] = mine.equal_slot;
+        scan_sh[3][warp] = mine.equal_new;
+    }
+    __syncthreads();
+    int pre[4], all[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int v = scan_sh[e][lane];
+        pre[e] = __reduce_add_sync(kAll, lane < warp ? v : 0);
+        all[e] = __reduce_add_sync(kAll, v);
+    }
+    if (ctas > 1) {
+        if (tid == 0) tot_sh = Counts{all[0], all[1], all[2], all[3]};
+        cluster.sync();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) all[e] = 0;
+        for (int c = 0; c < ctas; ++c) {
+            const Counts o = *cluster.map_shared_rank(&tot_sh, c);
+            const int v[4] = {o.below_slot, o.below_new, o.equal_slot, o.equal_new};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (c < rank) pre[e] += v[e];
+                all[e] += v[e];
+            }
         }
-    };
-    int n_gone = 0, n_new = 0, all_gone, all_new;
-    walk([&](int i, bool in, bool gone) {
-        n_gone += __popc(__ballot_sync(kAll, in && gone && i < len));
-        n_new += __popc(__ballot_sync(kAll, in && !gone && i >= len));
-    });
-    int gone0 = warp_prefix(n_gone, scan_sh, all_gone), new0 = warp_prefix(n_new, scan_sh, all_new);
+    }
+    // the last `ties` of the equal ones give way: those from the `stay`-th on
+    const int stay = all[2] + all[3] - ties;
+    int equal = pre[2] + pre[3];                                     // equal ones before
+    int gone = pre[0] + max(0, pre[2] - stay);                       // evicted slots before
+    const int all_gone = all[0] + max(0, all[2] - stay);
+    int entered = max(0, c0 - len) - pre[1] - max(0, equal - max(stay, pre[2]));   // new tokens that stay before
 
     // places for the new tokens, ascending: evicted slots, then empty ones
     int32_t *places = static_cast<int32_t *>(L.workspace) + (int64_t)h * L.total_tokens + t0;
-    for (int s = len + tid; s < keep; s += kSelThreads) places[all_gone + s - len] = s;
-    walk([&](int i, bool in, bool gone) {
-        const unsigned out = __ballot_sync(kAll, in && gone && i < len), enter = __ballot_sync(kAll, in && !gone && i >= len);
-        if (in && i < len) {
-            if (gone) {
-                places[gone0 + __popc(out & below)] = i;
-            } else if (L.w_out != L.w_in || L.pos_out != L.pos_in) {
+    for (int s = len + rank * kSelThreads + tid; s < keep; s += ctas * kSelThreads) places[all_gone + s - len] = s;
+    const unsigned lower = (1u << lane) - 1;
+    const bool copy = L.w_out != L.w_in || L.pos_out != L.pos_in;
+    walk([&](int i, bool in, uint32_t key) {
+        const bool slot = i < len;
+        const unsigned same = __ballot_sync(kAll, in && evict > 0 && key == tau);
+        const bool leaves = in && evict > 0 && (key < tau || (key == tau && equal + __popc(same & lower) >= stay));
+        equal += __popc(same);
+        const unsigned out = __ballot_sync(kAll, leaves && slot), enter = __ballot_sync(kAll, in && !leaves && !slot);
+        if (in && slot) {
+            if (leaves) {
+                places[gone + __popc(out & lower)] = i;
+            } else if (copy) {
                 L.w_out[base + i] = L.w_in[base + i];
                 L.pos_out[base + i] = L.pos_in[base + i];
             }
         } else if (in) {
-            L.slots[(t0 + i - len) * L.Hkv + h] = gone ? -1 : new0 + __popc(enter & below);   // a rank for now
+            L.slots[(t0 + i - len) * L.Hkv + h] = leaves ? -1 : entered + __popc(enter & lower);   // a rank for now
         }
-        gone0 += __popc(out);
-        new0 += __popc(enter);
+        gone += __popc(out);
+        entered += __popc(enter);
     });
-    __syncthreads();
-    for (int j = tid; j < m; j += kSelThreads) {
+    sync_all();
+    for (int64_t j = rank * kSelThreads + tid; j < m; j += ctas * kSelThreads) {
         int32_t *slot = L.slots + (t0 + j) * L.Hkv + h;
         const int r = *slot;
         if (r < 0) continue;
         const int s = places[r];
         *slot = s;
-        L.w_out[base + s] = new_weight(j);
+        L.w_out[base + s] = new_weight((int)j);
         L.pos_out[base + s] = (int32_t)(seen + j);
     }
 }
@@ -155,6 +243,7 @@ constexpr int kCopyWarps = 8;
 
 __global__ void __launch_bounds__(kCopyWarps * 32) cache_copy_kernel(const CacheInsertLaunch L, int64_t uniform_len) {
     const int b = blockIdx.y, lane = threadIdx.x & 31;
+    sm100::grid_dep_wait();
     int64_t t0;
     const int m = seq_rows(L.cu_seqlens, uniform_len, L.total_tokens, b, INT32_MAX, t0);
     const int64_t rows = (int64_t)m * L.Hkv;
@@ -187,13 +276,30 @@ size_t cache_insert_workspace(int64_t total_tokens, int Hkv) {
 
 cudaError_t launch_cache_insert(const CacheInsertLaunch &L, cudaStream_t stream) {
     const int64_t uniform_len = L.cu_seqlens ? 0 : L.total_tokens / L.num_seqs;
-    cache_select_kernel<<<L.num_seqs * L.Hkv, kSelThreads, 0, stream>>>(L, uniform_len);
-    cudaError_t e = cudaGetLastError();
+    // a cluster per (sequence, head) where its candidates, at the sequences'
+    // mean, are more than one CTA keeps
+    const int64_t candidates = L.capacity + (L.total_tokens + L.num_seqs - 1) / L.num_seqs;
+    int ctas = 1;
+    while (ctas < kMaxCluster && candidates > (int64_t)ctas * kKeep * kSelThreads) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(L.num_seqs * L.Hkv * ctas));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, cache_select_kernel, L, uniform_len);
     if (e != cudaSuccess) return e;
     int64_t x = (L.total_tokens * L.Hkv / L.num_seqs + kCopyWarps - 1) / kCopyWarps;
     x = x < 1 ? 1 : x > 4096 ? 4096 : x;
-    cache_copy_kernel<<<dim3((unsigned)x, L.num_seqs), kCopyWarps * 32, 0, stream>>>(L, uniform_len);
-    return cudaGetLastError();
+    cfg.gridDim = dim3((unsigned)x, L.num_seqs);
+    cfg.blockDim = dim3(kCopyWarps * 32);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, cache_copy_kernel, L, uniform_len);
 }
 
 }  // namespace gdn

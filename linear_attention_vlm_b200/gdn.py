@@ -9,6 +9,7 @@ back to, so a missing or unloadable libgdn.so raises immediately.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple
@@ -515,31 +516,32 @@ def gdn_swa_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
 MAX_TREE_NODES = 64
 
 
-def _check(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev, optional: bool = False) -> None:
+def _arg(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev) -> Optional[int]:
+    """The address of a contiguous tensor of this shape and type on ``dev``."""
     if t is None:
-        if optional:
-            return
         raise ValueError("%s is missing" % what)
-    if t.shape != shape or t.dtype != dtype or t.device != dev:
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
         raise ValueError("%s must be %s %s on %s" % (what, dtype, list(shape), dev))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr() or None
 
 
-def _check_cu(cu: Optional[torch.Tensor], B: int, dev, what: str = "cu_seqlens") -> None:
-    if cu is not None and (cu.dtype != torch.int32 or cu.device != dev or cu.shape != (B + 1,)):
-        raise ValueError("%s must be int32 [%d] on the same device" % (what, B + 1))
+def _opt(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev) -> Optional[int]:
+    return None if t is None else _arg(what, t, shape, dtype, dev)
 
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, dev) -> Tuple[torch.Tensor, int]:
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev), need
-    if workspace.device != dev:
-        raise ValueError("workspace must be on %s" % dev)
+        return torch.empty(need or 16, dtype=torch.uint8, device=dev), need
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on %s" % dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
 def _on_device(dev, fn, *args) -> int:
     """fn(*args, current stream of dev), with dev current."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
+    if dev.index == torch.cuda.current_device():
         return fn(*args, _stream(dev))
     with torch.cuda.device(dev):
         return fn(*args, _stream(dev))
@@ -548,13 +550,27 @@ def _on_device(dev, fn, *args) -> int:
 def _tree_nodes(max_nodes: Optional[int], cu: Optional[torch.Tensor], T: int, B: int) -> int:
     if max_nodes is not None:
         return int(max_nodes)
-    return max(1, min(MAX_TREE_NODES, T)) if cu is not None else max(1, T // B)
+    return max(1, min(MAX_TREE_NODES, T)) if cu is not None else max(1, T // max(B, 1))
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_attention_ws(*sizes: int) -> int:
+    return int(_load().gdn_tree_attention_workspace_size(*sizes))
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_weights_ws(*sizes: int) -> int:
+    return int(_load().gdn_cache_weights_workspace_size(*sizes))
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_insert_ws(*sizes: int) -> int:
+    return int(_load().gdn_cache_insert_workspace_size(*sizes))
 
 
 def gdn_tree_attention_workspace_size(num_seqs: int, total_nodes: int, max_nodes: int, capacity: int, Hq: int, Hkv: int,
                                       d: int = 128, dtype: torch.dtype = torch.bfloat16) -> int:
-    return int(_load().gdn_tree_attention_workspace_size(num_seqs, total_nodes, max_nodes, capacity, Hq, Hkv, d,
-                                                         _dtype_code(dtype)))
+    return _tree_attention_ws(num_seqs, total_nodes, max_nodes, capacity, Hq, Hkv, d, _dtype_code(dtype))
 
 
 def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parents: Optional[torch.Tensor],
@@ -573,35 +589,26 @@ def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent
     With cache_pos [B, Hkv, capacity] and seen [B] (int32) the window goes by
     token positions.  Returns (o [T, Hq, 128], lse [T, Hq] fp32)."""
     T, Hq, d = q.shape
-    dev = q.device
+    dev, dt = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("gdn_tree_attention needs CUDA tensors")
     B, cap, Hkv = k_cache.shape[:3]
-    dt = q.dtype
-    for name, t, shape in (("k", k, (T, Hkv, d)), ("v", v, (T, Hkv, d)), ("k_cache", k_cache, (B, cap, Hkv, d)),
-                           ("v_cache", v_cache, (B, cap, Hkv, d))):
-        _check(name, t, shape, dt, dev)
-    _check("parents", parents, (T,), torch.int32, dev, True)
-    _check("cache_lens", cache_lens, (B,), torch.int32, dev)
-    _check("cache_pos", cache_pos, (B, Hkv, cap), torch.int32, dev, True)
-    _check("seen", seen, (B,), torch.int32, dev, True)
-    _check_cu(cu_seqlens, B, dev)
     n = _tree_nodes(max_nodes, cu_seqlens, T, B)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _check("out", out, q.shape, dt, dev)
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    else:
-        _check("lse", lse, (T, Hq), torch.float32, dev)
     code = _dtype_code(dt)
-    lib = _load()
-    ws, ws_bytes = _scratch(workspace, lib.gdn_tree_attention_workspace_size(B, T, n, cap, Hq, Hkv, d, code), dev)
-    st = _on_device(dev, lib.gdn_tree_attention, _ptr(q), _ptr(k), _ptr(v), _ptr(parents), _ptr(cu_seqlens),
-                    _ptr(k_cache), _ptr(v_cache), _ptr(cache_lens), _ptr(cache_pos), _ptr(seen), _ptr(out), _ptr(lse),
-                    B, T, n, cap, Hq, Hkv, d, int(window), 0.0 if scale is None else float(scale), code, _ptr(ws),
-                    ws_bytes)
+    ws, ws_bytes = _scratch(workspace, _tree_attention_ws(B, T, n, cap, Hq, Hkv, d, code), dev)
+    i32, new, old = torch.int32, (T, Hkv, d), (B, cap, Hkv, d)
+    st = _on_device(
+        dev, _load().gdn_tree_attention, _arg("q", q, q.shape, dt, dev), _arg("k", k, new, dt, dev),
+        _arg("v", v, new, dt, dev), _opt("parents", parents, (T,), i32, dev),
+        _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), _arg("k_cache", k_cache, old, dt, dev),
+        _arg("v_cache", v_cache, old, dt, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
+        _opt("cache_pos", cache_pos, (B, Hkv, cap), i32, dev), _opt("seen", seen, (B,), i32, dev),
+        _arg("out", out, q.shape, dt, dev), _arg("lse", lse, (T, Hq), torch.float32, dev), B, T, n, cap, Hq, Hkv, d,
+        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes)
     if st != GDN_OK:
         raise GdnError(st, "gdn_tree_attention")
     return out, lse
@@ -616,24 +623,20 @@ def gdn_tree_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     [B, H, d, d] fp32; cu_seqlens int32 [B+1] or None (equal trees).  Returns
     out [T, H, d]."""
     T, H, d = q.shape
-    dev = q.device
+    dev, dt = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("gdn_tree_step needs CUDA tensors")
     B = state.shape[0]
-    _check("k", k, (T, H, d), q.dtype, dev)
-    _check("v", v, (T, H, d), q.dtype, dev)
-    _check("g", g, (T, H), torch.float32, dev)
-    _check("beta", beta, (T, H), torch.float32, dev)
-    _check("parents", parents, (T,), torch.int32, dev, True)
-    _check("state", state, (B, H, d, d), torch.float32, dev)
-    _check_cu(cu_seqlens, B, dev)
     n = _tree_nodes(max_nodes, cu_seqlens, T, B)
     if out is None:
         out = torch.empty_like(v)
-    else:
-        _check("out", out, (T, H, d), q.dtype, dev)
-    st = _on_device(dev, _load().gdn_tree_step, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parents),
-                    _ptr(state), _ptr(out), _ptr(cu_seqlens), B, T, n, H, d, d, _dtype_code(q.dtype))
+    i32, f32, rows = torch.int32, torch.float32, (T, H, d)
+    st = _on_device(
+        dev, _load().gdn_tree_step, _arg("q", q, rows, dt, dev), _arg("k", k, rows, dt, dev),
+        _arg("v", v, rows, dt, dev), _arg("g", g, (T, H), f32, dev), _arg("beta", beta, (T, H), f32, dev),
+        _opt("parents", parents, (T,), i32, dev), _arg("state", state, (B, H, d, d), f32, dev),
+        _arg("out", out, rows, dt, dev), _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, n, H, d, d,
+        _dtype_code(dt))
     if st != GDN_OK:
         raise GdnError(st, "gdn_tree_step")
     return out
@@ -641,8 +644,7 @@ def gdn_tree_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
 
 def gdn_cache_weights_workspace_size(num_seqs: int, total_queries: int, total_tokens: int, capacity: int, Hq: int,
                                      Hkv: int, d: int = 128, dtype: torch.dtype = torch.bfloat16) -> int:
-    return int(_load().gdn_cache_weights_workspace_size(num_seqs, total_queries, total_tokens, capacity, Hq, Hkv, d,
-                                                        _dtype_code(dtype)))
+    return _cache_weights_ws(num_seqs, total_queries, total_tokens, capacity, Hq, Hkv, d, _dtype_code(dtype))
 
 
 def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cache: torch.Tensor, weights: torch.Tensor,
@@ -659,35 +661,25 @@ def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cac
     [T, Hkv] fp32)."""
     Tq, Hq, d = q.shape
     T = k.shape[0]
-    dev = q.device
+    dev, dt = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("gdn_cache_weights needs CUDA tensors")
     B, cap, Hkv = k_cache.shape[:3]
-    dt = q.dtype
-    _check("lse", lse, (Tq, Hq), torch.float32, dev)
-    _check("k", k, (T, Hkv, d), dt, dev)
-    _check("k_cache", k_cache, (B, cap, Hkv, d), dt, dev)
-    _check("weights", weights, (B, Hkv, cap), torch.float32, dev)
-    _check("cache_lens", cache_lens, (B,), torch.int32, dev)
-    _check("cache_pos", cache_pos, (B, Hkv, cap), torch.int32, dev, True)
-    _check("seen", seen, (B,), torch.int32, dev, True)
-    _check_cu(cu_queries, B, dev, "cu_queries")
-    _check_cu(cu_tokens, B, dev, "cu_tokens")
     if weights_out is None:
         weights_out = weights
-    else:
-        _check("weights_out", weights_out, (B, Hkv, cap), torch.float32, dev)
     if new_weights is None:
         new_weights = torch.empty((T, Hkv), dtype=torch.float32, device=dev)
-    else:
-        _check("new_weights", new_weights, (T, Hkv), torch.float32, dev)
     code = _dtype_code(dt)
-    lib = _load()
-    ws, ws_bytes = _scratch(workspace, lib.gdn_cache_weights_workspace_size(B, Tq, T, cap, Hq, Hkv, d, code), dev)
-    st = _on_device(dev, lib.gdn_cache_weights, _ptr(q), _ptr(lse), _ptr(k), _ptr(k_cache), _ptr(weights),
-                    _ptr(weights_out), _ptr(new_weights), _ptr(cu_queries), _ptr(cu_tokens), _ptr(cache_lens),
-                    _ptr(cache_pos), _ptr(seen), B, Tq, T, cap, Hq, Hkv, d, int(window),
-                    0.0 if scale is None else float(scale), code, _ptr(ws), ws_bytes)
+    ws, ws_bytes = _scratch(workspace, _cache_weights_ws(B, Tq, T, cap, Hq, Hkv, d, code), dev)
+    i32, f32, cells = torch.int32, torch.float32, (B, Hkv, cap)
+    st = _on_device(
+        dev, _load().gdn_cache_weights, _arg("q", q, q.shape, dt, dev), _arg("lse", lse, (Tq, Hq), f32, dev),
+        _arg("k", k, (T, Hkv, d), dt, dev), _arg("k_cache", k_cache, (B, cap, Hkv, d), dt, dev),
+        _arg("weights", weights, cells, f32, dev), _arg("weights_out", weights_out, cells, f32, dev),
+        _arg("new_weights", new_weights, (T, Hkv), f32, dev), _opt("cu_queries", cu_queries, (B + 1,), i32, dev),
+        _opt("cu_tokens", cu_tokens, (B + 1,), i32, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
+        _opt("cache_pos", cache_pos, cells, i32, dev), _opt("seen", seen, (B,), i32, dev), B, Tq, T, cap, Hq, Hkv, d,
+        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes)
     if st != GDN_OK:
         raise GdnError(st, "gdn_cache_weights")
     return weights_out, new_weights
@@ -707,39 +699,31 @@ def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
     default to their inputs (in place).  Returns (weights_out, pos_out,
     lens_out, seen_out, slots [T, Hkv] int32, -1 where a token did not stay)."""
     T, Hkv, d = k.shape
-    dev = k.device
+    dev, dt = k.device, k.dtype
     if dev.type != "cuda":
         raise ValueError("gdn_cache_insert needs CUDA tensors")
     B, cap = k_cache.shape[:2]
-    for name, t, shape in (("v", v, (T, Hkv, d)), ("k_cache", k_cache, (B, cap, Hkv, d)),
-                           ("v_cache", v_cache, (B, cap, Hkv, d))):
-        _check(name, t, shape, k.dtype, dev)
-    _check_cu(cu_seqlens, B, dev)
-    _check("new_weights", new_weights, (T, Hkv), torch.float32, dev, True)
-    _check("slots", slots, (T, Hkv), torch.int32, dev, True)
-    weights_out = weights if weights_out is None else weights_out
-    pos_out = cache_pos if pos_out is None else pos_out
-    lens_out = cache_lens if lens_out is None else lens_out
-    seen_out = seen if seen_out is None else seen_out
-    for name, t, shape, dt in (("weights", weights, (B, Hkv, cap), torch.float32),
-                               ("weights_out", weights_out, (B, Hkv, cap), torch.float32),
-                               ("cache_pos", cache_pos, (B, Hkv, cap), torch.int32),
-                               ("pos_out", pos_out, (B, Hkv, cap), torch.int32),
-                               ("cache_lens", cache_lens, (B,), torch.int32), ("lens_out", lens_out, (B,), torch.int32),
-                               ("seen", seen, (B,), torch.int32), ("seen_out", seen_out, (B,), torch.int32)):
-        _check(name, t, shape, dt, dev)
     if slots is None:
         slots = torch.empty((T, Hkv), dtype=torch.int32, device=dev)
-    code = _dtype_code(k.dtype)
-    lib = _load()
-    ws, ws_bytes = _scratch(workspace, lib.gdn_cache_insert_workspace_size(B, T, cap, Hkv, d, code), dev)
-    st = _on_device(dev, lib.gdn_cache_insert, _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(weights),
-                    _ptr(weights_out), _ptr(cache_pos), _ptr(pos_out), _ptr(cache_lens), _ptr(lens_out), _ptr(seen),
-                    _ptr(seen_out), _ptr(new_weights), _ptr(slots), _ptr(cu_seqlens), B, T, cap, Hkv, d, int(recent),
-                    code, _ptr(ws), ws_bytes)
+    code = _dtype_code(dt)
+    ws, ws_bytes = _scratch(workspace, _cache_insert_ws(B, T, cap, Hkv, d, code), dev)
+    i32, f32, rows, cells = torch.int32, torch.float32, (T, Hkv, d), (B, Hkv, cap)
+    w, p = _arg("weights", weights, cells, f32, dev), _arg("cache_pos", cache_pos, cells, i32, dev)
+    ln, sn = _arg("cache_lens", cache_lens, (B,), i32, dev), _arg("seen", seen, (B,), i32, dev)
+    st = _on_device(
+        dev, _load().gdn_cache_insert, _arg("k", k, rows, dt, dev), _arg("v", v, rows, dt, dev),
+        _arg("k_cache", k_cache, (B, cap, Hkv, d), dt, dev), _arg("v_cache", v_cache, (B, cap, Hkv, d), dt, dev),
+        w, w if weights_out is None else _arg("weights_out", weights_out, cells, f32, dev),
+        p, p if pos_out is None else _arg("pos_out", pos_out, cells, i32, dev),
+        ln, ln if lens_out is None else _arg("lens_out", lens_out, (B,), i32, dev),
+        sn, sn if seen_out is None else _arg("seen_out", seen_out, (B,), i32, dev),
+        _opt("new_weights", new_weights, (T, Hkv), f32, dev), _arg("slots", slots, (T, Hkv), i32, dev),
+        _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, cap, Hkv, d, int(recent), code, ws.data_ptr(),
+        ws_bytes)
     if st != GDN_OK:
         raise GdnError(st, "gdn_cache_insert")
-    return weights_out, pos_out, lens_out, seen_out, slots
+    return (weights if weights_out is None else weights_out, cache_pos if pos_out is None else pos_out,
+            cache_lens if lens_out is None else lens_out, seen if seen_out is None else seen_out, slots)
 
 
 class _SessionBuffers(ctypes.Structure):
