@@ -33,6 +33,7 @@ constexpr int kKeep = 10;          // keys a thread holds: 10240 candidates a CT
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;     // the portable limit
 constexpr unsigned kAll = 0xffffffffu;
+constexpr uint32_t kProtected = 0xffffffffu, kZero = 0x80000000u;   // keys of recent positions and of weight 0
 
 // order-preserving bits of a weight; NaN below everything, -0 as 0
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -41,15 +42,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// One more in hist[digit] for every lane with `in`.  Weights are often alike
-// (zeros above all): the lanes that share the first lane's digit add once.
-__device__ __forceinline__ void count_digit(unsigned *hist, bool in, uint32_t digit) {
-    const unsigned act = __ballot_sync(kAll, in);
-    if (!act) return;
-    const int first = __ffs(act) - 1;
+// One more in hist[digit] for every lane of `on`.  Equal keys share a bin, so
+// the lanes that have the first lane's digit add once.
+__device__ __forceinline__ void count_digit(unsigned *hist, unsigned on, uint32_t digit) {
+    if (!on) return;
+    const int lane = threadIdx.x & 31, first = __ffs(on) - 1;
     const uint32_t lead = __shfl_sync(kAll, digit, first);
+    const bool in = on >> lane & 1;
     const unsigned same = __ballot_sync(kAll, in && digit == lead);
-    if ((int)(threadIdx.x & 31) == first) atomicAdd(&hist[lead], __popc(same));
+    if (lane == first) atomicAdd(&hist[lead], __popc(same));
     else if (in && digit != lead) atomicAdd(&hist[digit], 1u);
 }
 
@@ -79,13 +80,17 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
     const int C = len + m, keep = min(cap, C), evict = C - keep;
     const int64_t base = ((int64_t)b * L.Hkv + h) * cap;
     auto new_weight = [&](int j) { return L.w_new ? L.w_new[(t0 + j) * L.Hkv + h] : 0.f; };
+    const int32_t *pos_in = L.pos_in + base;
+    const float *w_in = L.w_in + base;
+    // positions above `old` are among the last `recent`
+    const int old = (int)max((int64_t)INT32_MIN, min((int64_t)INT32_MAX, seen + m - L.recent - 1));
     auto key_of = [&](int i) -> uint32_t {
         if (i < len) {
-            const int pos = L.pos_in[base + i];
-            const float w = L.w_in[base + i];
-            return seen + m - pos <= L.recent ? 0xffffffffu : weight_key(w);
+            const int pos = pos_in[i];
+            const float w = w_in[i];
+            return pos > old ? kProtected : weight_key(w);
         }
-        return C - i <= L.recent ? 0xffffffffu : weight_key(new_weight(i - len));
+        return C - i <= L.recent ? kProtected : weight_key(new_weight(i - len));
     };
     // a warp owns `rounds` x 32 consecutive candidates from c0 on, so ranks are running counts
     const int rounds = (int)(((int64_t)C + ctas * kSelThreads - 1) / (ctas * kSelThreads));
@@ -99,16 +104,21 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
             kept[k] = k < rounds && i < C ? key_of(i) : 0u;
         }
     }
-    // calls f(candidate, it exists, key) for the warp's candidates, all lanes together
+    // calls f(first candidate, mask of those that exist, key) for the warp's rounds, all lanes together
     auto walk = [&](auto f) {
+        const int left = C - c0;
 #pragma unroll
-        for (int k = 0; k < kKeep; ++k)
-            if (k < rounds) f(c0 + 32 * k + lane, c0 + 32 * k + lane < C, kept[k]);
-        for (int k = kKeep; k < rounds; ++k) {
+        for (int k = 0; k < kKeep; ++k) {
+            if (k >= rounds || 32 * k >= left) break;
+            f(c0 + 32 * k, left - 32 * k >= 32 ? kAll : (1u << (left - 32 * k)) - 1, kept[k]);
+        }
+        for (int k = kKeep; k < rounds && 32 * k < left; ++k) {
             const int i = c0 + 32 * k + lane;
-            f(i, i < C, evict > 0 && i < C ? key_of(i) : 0u);
+            f(c0 + 32 * k, left - 32 * k >= 32 ? kAll : (1u << (left - 32 * k)) - 1, evict > 0 && i < C ? key_of(i) : 0u);
         }
     };
+    // which of 32 candidates from i on are slots
+    auto slots_of = [&](int i) { return i + 32 <= len ? kAll : i >= len ? 0u : (1u << (len - i)) - 1; };
 
     // tau, and how many of the candidates equal to it give way
     uint32_t tau = 0;
@@ -119,11 +129,24 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
         int rest = evict;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            walk([&](int, bool in, uint32_t key) {
-                const bool on = in && (pass == 0 || key >> (shift + bits) == tau >> (shift + bits));
-                count_digit(hist[pass], on, (key >> shift) & (kBins - 1) & ((1u << bits) - 1));
-            });
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 1 ? 11 : 10;   // of the later passes
+            if (pass == 0) {
+                // the two keys that many candidates share are counted apart
+                int recents = 0, zeros = 0;
+                walk([&](int, unsigned in, uint32_t key) {
+                    const unsigned r = __ballot_sync(kAll, key == kProtected) & in, z = __ballot_sync(kAll, key == kZero) & in;
+                    recents += __popc(r);
+                    zeros += __popc(z);
+                    count_digit(hist[0], in & ~(r | z), key >> 21);
+                });
+                if (lane == 0 && recents) atomicAdd(&hist[0][kProtected >> 21], recents);
+                if (lane == 0 && zeros) atomicAdd(&hist[0][kZero >> 21], zeros);
+            } else {
+                walk([&](int, unsigned in, uint32_t key) {
+                    const unsigned on = __ballot_sync(kAll, (key ^ tau) >> (shift + bits) == 0) & in;
+                    count_digit(hist[pass], on, (key >> shift) & ((1u << bits) - 1));
+                });
+            }
             sync_all();
             // bins 2 tid, 2 tid + 1 of all CTAs, and what lies before them
             unsigned n0 = 0, n1 = 0;
@@ -159,12 +182,14 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
     // counts before this warp, over the cluster
     Counts mine = {0, 0, 0, 0};
     if (evict > 0)
-        walk([&](int i, bool in, uint32_t key) {
-            const bool slot = i < len;
-            mine.below_slot += __popc(__ballot_sync(kAll, in && slot && key < tau));
-            mine.below_new += __popc(__ballot_sync(kAll, in && !slot && key < tau));
-            mine.equal_slot += __popc(__ballot_sync(kAll, in && slot && key == tau));
-            mine.equal_new += __popc(__ballot_sync(kAll, in && !slot && key == tau));
+        walk([&](int i, unsigned in, uint32_t key) {
+            const unsigned below = __ballot_sync(kAll, key < tau) & in, same = __ballot_sync(kAll, key == tau) & in;
+            if (!(below | same)) return;
+            const unsigned slots = slots_of(i);
+            mine.below_slot += __popc(below & slots);
+            mine.below_new += __popc(below & ~slots);
+            mine.equal_slot += __popc(same & slots);
+            mine.equal_new += __popc(same & ~slots);
         });
     __syncthreads();
     if (lane == 0) {
@@ -208,21 +233,27 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
     for (int s = len + rank * kSelThreads + tid; s < keep; s += ctas * kSelThreads) places[all_gone + s - len] = s;
     const unsigned lower = (1u << lane) - 1;
     const bool copy = L.w_out != L.w_in || L.pos_out != L.pos_in;
-    walk([&](int i, bool in, uint32_t key) {
-        const bool slot = i < len;
-        const unsigned same = __ballot_sync(kAll, in && evict > 0 && key == tau);
-        const bool leaves = in && evict > 0 && (key < tau || (key == tau && equal + __popc(same & lower) >= stay));
-        equal += __popc(same);
-        const unsigned out = __ballot_sync(kAll, leaves && slot), enter = __ballot_sync(kAll, in && !leaves && !slot);
-        if (in && slot) {
-            if (leaves) {
+    walk([&](int i0, unsigned in, uint32_t key) {
+        unsigned leave = 0;
+        if (evict > 0) {
+            const unsigned same = __ballot_sync(kAll, key == tau) & in;
+            leave = __ballot_sync(kAll, key < tau) & in;
+            if (same) {
+                leave |= __ballot_sync(kAll, key == tau && equal + __popc(same & lower) >= stay) & in;
+                equal += __popc(same);
+            }
+        }
+        const unsigned slots = slots_of(i0) & in, out = leave & slots, enter = in & ~slots & ~leave;
+        const int i = i0 + lane;
+        if (slots >> lane & 1) {
+            if (out >> lane & 1) {
                 places[gone + __popc(out & lower)] = i;
             } else if (copy) {
-                L.w_out[base + i] = L.w_in[base + i];
-                L.pos_out[base + i] = L.pos_in[base + i];
+                L.w_out[base + i] = w_in[i];
+                L.pos_out[base + i] = pos_in[i];
             }
-        } else if (in) {
-            L.slots[(t0 + i - len) * L.Hkv + h] = leaves ? -1 : entered + __popc(enter & lower);   // a rank for now
+        } else if (in >> lane & 1) {
+            L.slots[(t0 + i - len) * L.Hkv + h] = leave >> lane & 1 ? -1 : entered + __popc(enter & lower);   // a rank for now
         }
         gone += __popc(out);
         entered += __popc(enter);
@@ -277,10 +308,13 @@ size_t cache_insert_workspace(int64_t total_tokens, int Hkv) {
 cudaError_t launch_cache_insert(const CacheInsertLaunch &L, cudaStream_t stream) {
     const int64_t uniform_len = L.cu_seqlens ? 0 : L.total_tokens / L.num_seqs;
     // a cluster per (sequence, head) where its candidates, at the sequences'
-    // mean, are more than one CTA keeps
+    // mean, are more than one CTA keeps, or where SMs would stay idle
     const int64_t candidates = L.capacity + (L.total_tokens + L.num_seqs - 1) / L.num_seqs;
+    const int64_t lists = (int64_t)L.num_seqs * L.Hkv;
     int ctas = 1;
-    while (ctas < kMaxCluster && candidates > (int64_t)ctas * kKeep * kSelThreads) ctas *= 2;
+    while (ctas < kMaxCluster && (candidates > (int64_t)ctas * kKeep * kSelThreads ||
+                                  (2 * ctas * lists <= 148 && candidates > 2048 * ctas)))
+        ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(L.num_seqs * L.Hkv * ctas));
     cfg.blockDim = dim3(kSelThreads);

@@ -61,10 +61,11 @@ template <bool ROWS> struct Cfg {
 };
 enum : int { B_QFULL = 0, B_QEMPTY, B_FIN, B_SFULL, B_PREADY = B_SFULL + 2, B_PVDONE = B_PREADY + 2, B_KFULL = B_PVDONE + 2,
              B_KEMPTY = B_KFULL + 3, B_VFULL = B_KEMPTY + 3, B_VEMPTY = B_VFULL + 3, B_NUM = B_VEMPTY + 3 };
-// after the barriers (offsets from kBar)
+// after the barriers (offsets from kBar); the exchange has 8 bytes a stream and
+// row: a value of each half in fp32, or two of each in bf16
 constexpr uint32_t kOffTmem = 8 * B_NUM, kOffAbort = kOffTmem + 4, kOffErr = kOffTmem + 8, kOffPlan = 192;
 constexpr uint32_t kOffPar = 256;                     // [2 streams][64] parents, int8
-constexpr uint32_t kOffXch = kOffPar + 128;           // [2 streams][2 halves][128] fp32
+constexpr uint32_t kOffXch = kOffPar + 128;           // [2 streams][128 rows] 8 bytes
 static_assert(kOffErr + 4 <= kOffPlan, "barrier area");
 static_assert(Cfg<false>::kBar + kOffXch + 2048 <= Cfg<false>::kSmem, "shared memory");
 static_assert(Cfg<true>::kBar + kOffXch + 2048 + 1024 <= Cfg<true>::kSmem, "shared memory");
@@ -385,16 +386,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sa = tm + lane_off + TM_S + x * kBN + 64 * half;
         const uint32_t oa = tm + lane_off + TM_O + x * kD + 64 * half;
         const float c = p.c;
-        float *xch = reinterpret_cast<float *>(ctl + kOffXch);            // [stream][half][128]
-        float *mine = xch + (x * 2 + half) * 128 + r, *other = xch + (x * 2 + (half ^ 1)) * 128 + r;
+        float *xch = reinterpret_cast<float *>(ctl + kOffXch);            // [stream][128 rows][2]
+        float *mine = xch + (x * 128 + r) * 2 + half, *other = xch + (x * 128 + r) * 2 + (half ^ 1);
         int8_t *par = reinterpret_cast<int8_t *>(ctl + kOffPar) + x * 64;
         const int bar_pair = 1 + 4 * x + quarter, bar_group = 9 + x, bar_both = 11;
-        auto partner = [&](float v) -> float {   // the other half's value of this row
+        // the sum of the halves' values of this row
+        auto pair_sum = [&](float v) -> float {
+            named_bar_sync(bar_pair, 64);
             *mine = v;
             named_bar_sync(bar_pair, 64);
-            const float got = *other;
+            return v + *other;
+        };
+        // the larger of the halves' values as bf16: m only has to be the same in
+        // both halves and within a factor of the maximum (two parities keep
+        // consecutive exchanges apart)
+        __nv_bfloat16 *mx_sh = reinterpret_cast<__nv_bfloat16 *>(xch) + (x * 128 + r) * 4;   // [2 parities][2 halves]
+        int parity = 0;
+        auto pair_max = [&](float v) -> float {
+            const __nv_bfloat16 w = __float2bfloat16_rn(v);
+            __nv_bfloat16 *at = mx_sh + 2 * parity;
+            parity ^= 1;
+            at[half] = w;
             named_bar_sync(bar_pair, 64);
-            return got;
+            return fmaxf(__bfloat162float(w), __bfloat162float(at[half ^ 1]));
         };
         int used = 0, cnt = 0;                   // key blocks so far; blocks of this stream so far
         bool ok = true;
@@ -440,6 +454,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             // only keys at positions above `far` are inside the window
             const int32_t *pos = p.window && p.pos ? p.pos + ((int64_t)seg.b * p.Hkv + seg.h) * p.capacity : nullptr;
             const int far = p.window ? (pos ? p.seen[seg.b] : seg.s.len) + depth - p.window : INT32_MIN;
+            // positions of this half's keys, two a lane, fetched a block ahead
+            int p0 = INT32_MAX, p1 = INT32_MAX;
+            auto fetch_pos = [&](int jj) {
+                p0 = p1 = INT32_MAX;
+                if (!pos || !work || jj >= nblk || seg.draft(seg.blk0 + jj)) return;
+                const int k0 = seg.key0(seg.blk0 + jj) + 64 * half;
+                if (k0 + lane < seg.s.len) p0 = pos[k0 + lane];
+                if (k0 + 32 + lane < seg.s.len) p1 = pos[k0 + 32 + lane];
+            };
+            fetch_pos(ROWS ? 0 : x);
+            const int top = p.window ? __reduce_max_sync(kAll, vrow ? far : INT32_MIN) : 0;   // the warp's last masked position
             float m = -INFINITY, l = 0.f;   // m: the same in both halves of a row; l: this half's share
             for (int jj = ROWS ? 0 : x; jj < nblk; jj += ROWS ? 1 : 2) {
                 const int j = seg.blk0 + jj, valid = seg.valid(j);
@@ -451,10 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int left = valid - 64 * half, k0 = seg.key0(j) + 64 * half;
                     vis = left >= 64 ? ~0ull : left <= 0 ? 0 : (1ull << left) - 1;
                     if (p.window && work) {
-                        const int top = __reduce_max_sync(kAll, vrow ? far : INT32_MIN);
                         if (pos) {
-                            const int p0 = lane < left ? pos[k0 + lane] : INT32_MAX;
-                            const int p1 = lane + 32 < left ? pos[k0 + 32 + lane] : INT32_MAX;
                             if (__reduce_min_sync(kAll, min(p0, p1)) <= top) {
                                 uint32_t lo = 0, hi = 0;
                                 for (int i = 0; i < 32; ++i) {
@@ -469,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                if (pos) fetch_pos(jj + (ROWS ? 1 : 2));
                 wait(B_SFULL + x, cnt & 1, 89);
                 ++cnt;
                 tc_fence_after();
@@ -491,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
                     }
-                    const float mb = fmaxf(mx, partner(mx)) * c;
+                    const float mb = pair_max(mx) * c;
                     float alpha = 1.f;
                     bool rescale = false;
                     if (mb > m + kRescaleThreshold) {   // also taken when m is still -inf
@@ -582,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(B_PVDONE + x, (cnt - 1) & 1, 91);
                 tc_fence_after();
                 if (work) {
-                    const float lsum = l + partner(l);
+                    const float lsum = pair_sum(l);
                     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
 #pragma unroll 1
                     for (int c4 = 0; c4 < 2; ++c4) {
@@ -596,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // merge the streams: each takes 32 of the half's 64 columns
                 const bool two = nblk > 1;
                 if (x == 0 || two) wait(B_PVDONE + x, (cnt - 1) & 1, 92);
-                const float lrow = work ? l + partner(l) : 0.f;   // a stream without blocks: m = -inf, l = 0
+                const float lrow = work ? pair_sum(l) : 0.f;   // a stream without blocks: m = -inf, l = 0
                 tc_fence_before();
                 named_bar_sync(bar_both, 32 * kSoftmaxWarps);     // both streams' products have completed
                 tc_fence_after();
@@ -604,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else *mine = lrow;
                 named_bar_sync(bar_both, 32 * kSoftmaxWarps);
                 if (work) {
-                    const float m0 = xch[r], l0 = xch[128 + r], m1 = xch[256 + r], l1 = xch[384 + r];
+                    const float m0 = xch[2 * r], l0 = xch[2 * r + 1], m1 = xch[256 + 2 * r], l1 = xch[257 + 2 * r];
                     const float mm = fmaxf(m0, m1);
                     const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
                     const float ll = f0 * l0 + f1 * l1, inv = ll > 0.f ? 1.f / ll : 0.f;
@@ -650,8 +673,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Params
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr unsigned kAll = 0xffffffffu;
     constexpr int kRows = Cfg<ROWS>::kTiles * kBM;
+    const int part = warp % width, b = blockIdx.y;
+    const int64_t at_row = (int64_t)blockIdx.x * (kJoinWarps / width) + warp / width;   // (node, head) of the sequence
+    const int64_t node = at_row / p.Hq;
+    const int hq = (int)(at_row % p.Hq), h = hq / p.group;
+    const Seq s = load_seq<ROWS>(p, b);
+    const int64_t row = s.bos * p.Hq + at_row;
+    const bool here = node < s.n;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, l = 0.f;
+    bool split = false;
     grid_dep_wait();
-    if (blockIdx.x == 0) {
+    if (blockIdx.x == 0 && b == 0) {
         if (tid == 0) bad = 0;
         __syncthreads();
         for (int i = tid; i < ctas; i += blockDim.x)
@@ -659,52 +692,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Params
         __syncthreads();
         if (tid == 0) *status = bad;
     }
-    const int part = warp % width;
-    const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / width) + warp / width;   // (node, head)
-    const int64_t t = row / p.Hq;
-    const int hq = (int)(row % p.Hq), h = hq / p.group;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = -INFINITY, l = 0.f;
-    bool split = false;
-    if (t < p.total) {
-        // the sequence that holds node t
-        int b = 0;
-        if (p.cu) {
-            int hi = p.num_seqs;   // cu[b] <= t < cu[hi]
-            while (hi - b > 1) {
-                const int mid = (b + hi) >> 1;
-                if (p.cu[mid] <= t) b = mid;
-                else hi = mid;
-            }
-        } else {
-            b = (int)(t / p.uniform_len);
-        }
-        const Seq s = load_seq<ROWS>(p, b);
-        const int64_t node = t - s.bos;
-        if (node >= 0 && node < s.n) {
-            const int tile = (int)node / p.tile_nodes, it = ROWS ? tile / 2 : tile;
-            const int r = (ROWS ? (tile & 1) * kBM : 0) + ((int)node % p.tile_nodes) * p.group + hq % p.group;
-            const int64_t W = p.prefix[p.num_seqs], runs = min((int64_t)ctas, W);
-            const int64_t start = p.prefix[b] + ((int64_t)h * s.items + it) * s.blocks, last = start + s.blocks - 1;
-            const int c0 = (int)(((start + 1) * runs - 1) / W), c1 = (int)(((last + 1) * runs - 1) / W);
-            split = c1 > c0;
-            if (split) {
-                auto at = [&](int c) { return (int64_t)(c == c0 ? 2 * c + 1 : 2 * c) * kRows + r; };
-                for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ml[at(c)].x);
+    if (here) {
+        const int tile = (int)node / p.tile_nodes, it = ROWS ? tile / 2 : tile;
+        const int r = (ROWS ? (tile & 1) * kBM : 0) + ((int)node % p.tile_nodes) * p.group + hq % p.group;
+        const int64_t W = p.prefix[p.num_seqs], runs = min((int64_t)ctas, W);
+        const int64_t start = p.prefix[b] + ((int64_t)h * s.items + it) * s.blocks, last = start + s.blocks - 1;
+        const int c0 = (int)(((start + 1) * runs - 1) / W), c1 = (int)(((last + 1) * runs - 1) / W);
+        split = c1 > c0;
+        if (split) {
+            auto at = [&](int c) { return (int64_t)(c == c0 ? 2 * c + 1 : 2 * c) * kRows + r; };
+            for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ml[at(c)].x);
 #pragma unroll
-                for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-#pragma unroll 4
-                for (int c = c0 + part; c <= c1; c += width) {
-                    const int64_t i = at(c);
-                    const float2 ml = p.ml[i];
-                    const float4 v = reinterpret_cast<const float4 *>(p.part)[i * 32 + lane];
-                    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-                    l = fmaf(f, ml.y, l);
-                    acc.x = fmaf(f, v.x, acc.x);
-                    acc.y = fmaf(f, v.y, acc.y);
-                    acc.z = fmaf(f, v.z, acc.z);
-                    acc.w = fmaf(f, v.w, acc.w);
-                }
+            for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+#pragma unroll 8
+            for (int c = c0 + part; c <= c1; c += width) {
+                const int64_t i = at(c);
+                const float2 ml = p.ml[i];
+                const float4 v = reinterpret_cast<const float4 *>(p.part)[i * 32 + lane];
+                const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+                l = fmaf(f, ml.y, l);
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
             }
         }
     }
@@ -795,9 +805,9 @@ template <bool ROWS> cudaError_t launch(const TreeAttnLaunch &L, cudaStream_t st
     // few items are cut many times: then a whole block joins a row
     const int64_t items = (int64_t)L.num_seqs * L.Hkv * (ROWS ? ((L.max_nodes + nodes - 1) / nodes + 1) / 2 : 1);
     const int width = items * 8 <= ctas ? kJoinWarps : 1;
-    const int64_t per = kJoinWarps / width, blocks = (L.total_nodes * L.Hq + per - 1) / per;
+    const int64_t per = kJoinWarps / width, blocks = ((int64_t)L.max_nodes * L.Hq + per - 1) / per;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)L.num_seqs);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
