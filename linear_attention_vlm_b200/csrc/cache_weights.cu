@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             auto load_q = [&](int c) -> bool {
                 const int s = loads % kQSlots;
-                if (loads >= kQSlots && !mbar_wait(bar(B_QEMPTY + s), ((loads - kQSlots) / kQSlots) & 1, lim, abort_flag)) {
+                if (loads >= kQSlots && !wait_phase(bar(B_QEMPTY + s), ((loads - kQSlots) / kQSlots) & 1, lim, abort_flag)) {
                     fail(101);
                     return false;
                 }
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = seg.blk0; ok && j < seg.blk1; j += 2) {
                     for (int x = 0; x < 2 && j + x < seg.blk1; ++x, ++keys) {
                         const int s = keys % kKStages;
-                        if (keys >= kKStages && !mbar_wait(bar(B_KEMPTY + s), ((keys - kKStages) / kKStages) & 1, lim, abort_flag)) {
+                        if (keys >= kKStages && !wait_phase(bar(B_KEMPTY + s), ((keys - kKStages) / kKStages) & 1, lim, abort_flag)) {
                             fail(102);
                             ok = false;
                             break;
@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int zero = 0;   // no copy may still be landing in shared memory at exit
             for (int s = 0; s < kKStages; ++s)
-                if (issued_k[s]) mbar_wait(bar(B_KFULL + s), (issued_k[s] - 1) & 1, drain, &zero);
+                if (issued_k[s]) wait_phase(bar(B_KFULL + s), (issued_k[s] - 1) & 1, drain, &zero);
             for (int s = 0; s < kQSlots; ++s)
-                if (issued_q[s]) mbar_wait(bar(B_QFULL + s), (issued_q[s] - 1) & 1, drain, &zero);
+                if (issued_q[s]) wait_phase(bar(B_QFULL + s), (issued_q[s] - 1) & 1, drain, &zero);
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int keys = 0, loads = 0, cnt[2] = {0, 0};   // cnt: products per stream
             bool ok = true;
             auto wait = [&](int b, uint32_t parity, int code) {
-                if (!mbar_wait(bar(b), parity, lim, abort_flag)) {
+                if (!wait_phase(bar(b), parity, lim, abort_flag)) {
                     fail(code);
                     ok = false;
                 }
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mma_commit(bar(B_FIN));   // every issued MMA completes before TMEM is released
             const int zero = 0;
-            mbar_wait(bar(B_FIN), 0, drain, &zero);
+            wait_phase(bar(B_FIN), 0, drain, &zero);
         }
     } else {
         // ------------------------------------------------------------ sums (warps 0-15)
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int first = s.m - s.nq + c * p.chunk_q, last = first + rows / p.group - 1;
                     // whether every row sees every key of the warp
                     const bool all = (old || kmax <= first) && (p.window == INT32_MAX || (int64_t)last - kmin < p.window);
-                    if (!__all_sync(kAll, mbar_wait(bar(B_SFULL + 2 * x + buf), (cnt >> 1) & 1, lim, abort_flag))) {
+                    if (!__all_sync(kAll, wait_phase(bar(B_SFULL + 2 * x + buf), (cnt >> 1) & 1, lim, abort_flag))) {
                         fail(106);
                         ok = false;
                     }

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "gdn_internal.h"
+#include "sm100.cuh"
 
 namespace gdn {
 
@@ -25,6 +26,40 @@ __device__ __forceinline__ int cached_slots(const int32_t *lens, int64_t capacit
     if (capacity == 0) return 0;
     const int n = lens[b];
     return n < 0 ? 0 : (n > capacity ? (int)capacity : n);
+}
+
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {   // never suspends the thread
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// sm100::mbar_wait, with two differences: a limit of 0 gives up at once where
+// the phase is not complete (try_wait alone may suspend for longer than a
+// copy takes), and the clock is read only once a wait has become long.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, const volatile int *abort) {
+    if (limit_ns == 0) return mbar_test_wait(bar, parity);
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        if (sm100::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+    }
+    return sm100::mbar_wait(bar, parity, limit_ns, abort);
+}
+
+// True in one lane of a converged warp.  The issuing warps run their loops with
+// all lanes and elect one per batch of instructions: addresses and descriptors
+// then stay in uniform registers, where a branch on the lane number would move
+// every operand of every product there (about 100 cycles a product).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Parent of node i (of a tree whose first row is bos): -1, or an index below

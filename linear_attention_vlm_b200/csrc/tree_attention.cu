@@ -15,18 +15,21 @@
 // CTA takes an equal run of them, whatever the lengths; an item that crosses
 // CTAs leaves partial sums that a second kernel joins.
 //
-// Two streams keep the tensor pipe and the copies busy while a softmax runs,
-// each with its own scores, accumulator, maximum and 8 softmax warps:
-//   by keys (trees of at most one tile): the streams take alternate key
-//     blocks of the same rows and are merged at the end;
-//   by rows (larger trees): the streams take two row tiles of the same key
+// A block is worked on in halves of 64 keys.  Two streams keep the tensor pipe
+// and the copies busy while a softmax runs, each with its own accumulator,
+// maximum and row sum and two score buffers of 64 columns:
+//   by keys (trees of at most one tile): stream x takes half x of every block
+//     for the same rows, and the streams are merged at the end;
+//   by rows (larger trees): the streams take two row tiles of the same half
 //     block, so a block is loaded once for 256 rows.
-//   warps 0-7 / 8-15  softmax of stream 0 / 1 (warps w and w + 4 split the
-//                     columns of the rows of TMEM lane quarter w % 4)
-//   warp 16           TMA producer: Q per item, K and V through rings
-//   warp 17           MMA issuer (one lane)
-// Tensor memory: S_0, S_1, O_0, O_1, 128 columns each; the bf16 P of a block
-// lies over the columns of its S, read by then.
+// With two buffers the scores of the next half are formed while the softmax of
+// this one runs, so the softmax warps hardly wait; a thread holds a whole row of
+// 64 scores in registers, so a row needs no exchange and its scores are read once.
+//   warps 0-3 / 4-7   softmax of stream 0 / 1 (a thread per row)
+//   warp 8            TMA producer: Q per item, K and V through rings
+//   warp 9            MMA issuer (one lane)
+// Tensor memory: per stream 2 x 64 columns of scores and 128 of output; the bf16
+// P of a half block lies over the columns of its S, read by then.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -49,8 +52,12 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.f;   // log2 units, as in the window attention
 constexpr int kMaxCtas = 160;
 
-constexpr int kSoftmaxWarps = 16, kProducerWarp = 16, kMmaWarp = 17;
-constexpr int kThreads = 32 * 18;
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 32 * 10;
+constexpr int kSub = 64;                // keys of a half block
+// Planning weight of an item beside its key blocks: starting one (its Q, the
+// first scores) and ending it (merge and stores) take about a block's time.
+constexpr int kItemCost = 1;
 
 // shared memory: [Q tiles][K ring][V ring][barriers][exchange]
 template <bool ROWS> struct Cfg {
@@ -59,25 +66,52 @@ template <bool ROWS> struct Cfg {
     static constexpr uint32_t kQ = 0, kK = kTiles * kBlk, kV = kK + kStages * kBlk, kBar = kV + kStages * kBlk;
     static constexpr size_t kSmem = 232448;           // the per-CTA maximum; the rest is alignment slack
 };
-enum : int { B_QFULL = 0, B_QEMPTY, B_FIN, B_SFULL, B_PREADY = B_SFULL + 2, B_PVDONE = B_PREADY + 2, B_KFULL = B_PVDONE + 2,
-             B_KEMPTY = B_KFULL + 3, B_VFULL = B_KEMPTY + 3, B_VEMPTY = B_VFULL + 3, B_NUM = B_VEMPTY + 3 };
-// after the barriers (offsets from kBar); the exchange has 8 bytes a stream and
-// row: a value of each half in fp32, or two of each in bf16
-constexpr uint32_t kOffTmem = 8 * B_NUM, kOffAbort = kOffTmem + 4, kOffErr = kOffTmem + 8, kOffPlan = 192;
-constexpr uint32_t kOffPar = 256;                     // [2 streams][64] parents, int8
-constexpr uint32_t kOffXch = kOffPar + 128;           // [2 streams][128 rows] 8 bytes
+// A parity wait tells a phase only from the one before it, so what a softmax
+// may run two half blocks ahead of has a barrier per score buffer (+ 2 stream + buffer).
+enum : int { B_QFULL = 0, B_QEMPTY = 2, B_FIN = 4, B_SFULL = 5, B_PREADY = 9, B_PVDONE = 13, B_KFULL = 17, B_KEMPTY = 20,
+             B_VFULL = 23, B_VEMPTY = 26, B_NUM = 29 };
+// after the barriers (offsets from kBar)
+constexpr uint32_t kOffTmem = 8 * B_NUM, kOffAbort = kOffTmem + 4, kOffErr = kOffTmem + 8, kOffPlan = 256;
+constexpr uint32_t kOffPar = 320;                     // [2 streams][64] parents, int8
+constexpr uint32_t kOffXch = kOffPar + 128;           // [2 streams][128 rows] maximum and row sum
+constexpr uint32_t kCtlBytes = kOffXch + 2048;
 static_assert(kOffErr + 4 <= kOffPlan, "barrier area");
-static_assert(Cfg<false>::kBar + kOffXch + 2048 <= Cfg<false>::kSmem, "shared memory");
-static_assert(Cfg<true>::kBar + kOffXch + 2048 + 1024 <= Cfg<true>::kSmem, "shared memory");
+static_assert(Cfg<false>::kBar + kCtlBytes <= Cfg<false>::kSmem, "shared memory");
+static_assert(Cfg<true>::kBar + kCtlBytes + 1024 <= Cfg<true>::kSmem, "shared memory");
 
 constexpr uint32_t TM_S = 0, TM_O = 256, kTmemCols = 512;   // + 128 * stream
+
+// 32 lanes x 64 consecutive fp32 columns; waits for completion.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,"
+        "%61,%62,%63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 struct Params {
     __nv_bfloat16 *o;
     float *lse;
     const int32_t *parents, *cu, *lens, *pos, *seen;
     int64_t uniform_len, total, capacity;
-    int num_seqs, max_nodes, Hq, Hkv, group, tile_nodes, window;
+    int num_seqs, max_nodes, Hq, Hkv, group, window;
+    int tile_nodes;                     // nodes of a row tile
+    int box_nodes, q_bufs;              // nodes of a copy of Q; buffers for it
     float c;                            // scale * log2(e)
     float *part;                        // [2 * CTAs][rows][128] partial sums
     float2 *ml;                         // [2 * CTAs][rows] their maxima (log2) and row sums
@@ -90,7 +124,8 @@ struct Params {
 struct Seq {
     int64_t bos;
     int n, len, kstart, blocks, tiles, items;
-    __device__ __forceinline__ int64_t work(int Hkv) const { return (int64_t)Hkv * items * blocks; }
+    __device__ __forceinline__ int cost() const { return blocks + kItemCost; }   // of an item
+    __device__ __forceinline__ int64_t work(int Hkv) const { return (int64_t)Hkv * items * cost(); }
 };
 
 template <bool ROWS> __device__ __forceinline__ Seq load_seq(const Params &p, int b) {
@@ -106,37 +141,63 @@ template <bool ROWS> __device__ __forceinline__ Seq load_seq(const Params &p, in
     return s;
 }
 
-// A CTA's run of key blocks, cut into segments of one item each.
+// A CTA's run of work units, cut into segments of one item each.  The first
+// kItemCost units of an item stand for its overhead, the others for its key blocks.
 template <bool ROWS> struct Walk {
     const Params &p;
-    int64_t w, end, base;   // base: blocks before sequence b
+    int64_t w, end, base;   // base: units before sequence b
     int b;
-    Seq s;
+    Seq s, after;           // of sequences b and b + 1, fetched ahead
     int h, it, blk0, blk1;  // the segment: key blocks [blk0, blk1) of item (h, it)
-    __device__ Walk(const Params &p_, int64_t w_, int64_t end_, int b_, int64_t base_) : p(p_), w(w_), end(end_), base(base_), b(b_) {
-        if (w < end) s = load_seq<ROWS>(p, b);
+    __device__ Walk(const Params &p_, int64_t w_, int64_t end_, int b_, int64_t base_, const Seq &s_)
+        : p(p_), w(w_), end(end_), base(base_), b(b_), s(s_) {
+        after = load_seq<ROWS>(p, min(b + 1, p.num_seqs - 1));
     }
     __device__ __forceinline__ bool next() {
-        if (w >= end) return false;
-        int64_t share;
-        while (w >= base + (share = s.work(p.Hkv))) {
-            base += share;
-            s = load_seq<ROWS>(p, ++b);
+        while (w < end) {
+            int64_t share;
+            while (w >= base + (share = s.work(p.Hkv))) {
+                base += share;
+                ++b;
+                s = after;
+                after = load_seq<ROWS>(p, min(b + 1, p.num_seqs - 1));
+            }
+            const int cost = s.cost();
+            const uint32_t off = (uint32_t)(w - base), item = off / cost;
+            h = (int)(item / s.items);
+            it = (int)(item % s.items);
+            const int at = (int)(off - item * cost);
+            const int upto = (int)min((int64_t)cost, at + (end - w));
+            w += upto - at;
+            blk0 = max(0, at - kItemCost);
+            blk1 = upto - kItemCost;
+            if (blk0 < blk1) return true;
         }
-        const int64_t off = w - base, item = off / s.blocks;
-        h = (int)(item / s.items);
-        it = (int)(item % s.items);
-        blk0 = (int)(off - item * s.blocks);
-        blk1 = (int)min((int64_t)s.blocks, blk0 + (end - w));
-        w += blk1 - blk0;
-        return true;
+        return false;
     }
     __device__ __forceinline__ bool draft(int j) const { return j == s.blocks - 1; }
     __device__ __forceinline__ int key0(int j) const { return s.kstart + j * kBN; }
     __device__ __forceinline__ int valid(int j) const { return draft(j) ? s.n : min(kBN, s.len - key0(j)); }
+    __device__ __forceinline__ int tiles() const { return ROWS ? min(2, s.tiles - 2 * it) : 1; }   // of the item
 };
 
-// CTA c of N takes blocks [c W / N, (c + 1) W / N); with N <= W no run is empty.
+// The half blocks of a segment, in order: by rows both streams take half h of
+// block j; by keys stream x takes half x of block j, if that has keys.
+template <bool ROWS> struct Halves {
+    int j, h;
+    __device__ __forceinline__ int half(int x) const { return ROWS ? h : x; }
+    __device__ __forceinline__ bool has(const Walk<ROWS> &seg, int x) const {
+        return ROWS ? x < seg.tiles() : kSub * x < seg.valid(j);
+    }
+    __device__ __forceinline__ bool last(const Walk<ROWS> &seg) const { return !ROWS || h == 1 || seg.valid(j) <= kSub; }   // of its block
+    __device__ __forceinline__ void step(const Walk<ROWS> &seg) {
+        if (last(seg)) ++j, h = 0;
+        else h = 1;
+    }
+    __device__ __forceinline__ bool done(const Walk<ROWS> &seg) const { return j >= seg.blk1; }
+};
+
+// CTA c of N takes units [c W / N, (c + 1) W / N); with N <= W no run is empty.
 __device__ __forceinline__ int64_t run_start(int64_t W, int c, int N) { return W * c / N; }
 
 template <bool ROWS>
@@ -151,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     constexpr unsigned kAll = 0xffffffffu;
     grid_dep_launch();
-    if (pad + C::kBar + kOffXch + 2048 > C::kSmem) {   // cannot happen with an aligned dynamic base
+    if (pad + C::kBar + kCtlBytes > C::kSmem) {   // cannot happen with an aligned dynamic base
         if (tid == 0) p.err[cta] = 80;
         return;
     }
@@ -165,24 +226,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicCAS(err_sh, 0, code);
     };
 
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    if (tid == 32 * kProducerWarp) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_QFULL + i), 1);
+            mbar_init(bar(B_QEMPTY + i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(B_PVDONE + i), 1);
+            mbar_init(bar(B_SFULL + i), 1);
+            mbar_init(bar(B_PREADY + i), 32 * kSoftmaxWarps / 2);
+        }
+        mbar_init(bar(B_FIN), 1);
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(bar(B_KFULL + s), 1);
+            mbar_init(bar(B_KEMPTY + s), 1);
+            mbar_init(bar(B_VFULL + s), 1);
+            mbar_init(bar(B_VEMPTY + s), 1);
+        }
+        *abort_flag = 0;
+        *err_sh = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&mQ);
+        tma_prefetch_desc(&mKc);
+        tma_prefetch_desc(&mVc);
+        tma_prefetch_desc(&mKn);
+        tma_prefetch_desc(&mVn);
+    }
+
     // ---------------------------------------------------------------- plan
-    // total blocks, then the sequence that this CTA's run starts in
-    int64_t *plan = reinterpret_cast<int64_t *>(ctl + kOffPlan);                // W, base of the first sequence, its index
-    int64_t *wsum = reinterpret_cast<int64_t *>(sm);                            // [18] scratch before any copy lands
-    int64_t W = 0;
-    for (int b = tid; b < p.num_seqs; b += kThreads) W += load_seq<ROWS>(p, b).work(p.Hkv);
+    // total units, then the sequence that this CTA's run starts in
+    int64_t *plan = reinterpret_cast<int64_t *>(ctl + kOffPlan);                // units before the first sequence, its index
+    Seq *plan_seq = reinterpret_cast<Seq *>(plan + 2);
+    int64_t *wsum = reinterpret_cast<int64_t *>(sm);                            // [10] scratch before any copy lands
+    static_assert(16 + sizeof(Seq) <= kOffPar - kOffPlan, "plan area");
+    int64_t W = 0, w0 = 0, w1 = 0;
+    const bool one_pass = p.num_seqs <= kThreads;
+    if (!one_pass) {   // the total first
+        for (int b = tid; b < p.num_seqs; b += kThreads) W += load_seq<ROWS>(p, b).work(p.Hkv);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(kAll, W, o);
-    if (lane == 0) wsum[warp] = W;
-    __syncthreads();
-    W = 0;
-    for (int i = 0; i < kThreads / 32; ++i) W += wsum[i];
-    const int runs = (int)min((int64_t)gridDim.x, W);
-    const int64_t w0 = cta < runs ? run_start(W, cta, runs) : W, w1 = cta < runs ? run_start(W, cta + 1, runs) : W;
+        for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(kAll, W, o);
+        if (lane == 0) wsum[warp] = W;
+        __syncthreads();
+        W = 0;
+        for (int i = 0; i < kThreads / 32; ++i) W += wsum[i];
+    }
+    auto my_run = [&] {
+        const int runs = (int)min((int64_t)gridDim.x, W);
+        w0 = cta < runs ? run_start(W, cta, runs) : W;
+        w1 = cta < runs ? run_start(W, cta + 1, runs) : W;
+    };
+    my_run();
     int64_t carry = 0;
     for (int b0 = 0; b0 < p.num_seqs && (carry <= w0 || cta == 0); b0 += kThreads) {
         const int b = b0 + tid;
-        const int64_t mine = b < p.num_seqs ? load_seq<ROWS>(p, b).work(p.Hkv) : 0;
+        Seq s;
+        int64_t mine = 0;
+        if (b < p.num_seqs) {
+            s = load_seq<ROWS>(p, b);
+            mine = s.work(p.Hkv);
+        }
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -193,68 +299,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 31) wsum[warp] = incl;
         __syncthreads();
         int64_t before = carry;
-        for (int i = 0; i < warp; ++i) before += wsum[i];
-        for (int i = 0; i < kThreads / 32; ++i) carry += wsum[i];
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += wsum[i];
+            carry += wsum[i];
+        }
+        if (one_pass) {
+            W = carry;
+            my_run();
+        }
         const int64_t start = before + incl - mine;
         if (mine > 0 && start <= w0 && w0 < start + mine) {
             plan[0] = start;
             plan[1] = b;
+            *plan_seq = s;
         }
         if (cta == 0 && b < p.num_seqs) p.prefix[b] = start;
     }
     if (cta == 0 && tid == 0) p.prefix[p.num_seqs] = W;
-    if (w0 == w1) {   // nothing for this CTA
-        if (tid == 0) p.err[cta] = 0;
-        return;
-    }
-
-    if (warp == 0) {
-        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-        tmem_relinquish();
-    }
-    if (tid == 32 * kProducerWarp) {
-        mbar_init(bar(B_QFULL), 1);
-        mbar_init(bar(B_QEMPTY), 1);
-        mbar_init(bar(B_FIN), 1);
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(bar(B_SFULL + x), 1);
-            mbar_init(bar(B_PREADY + x), 32 * kSoftmaxWarps / 2);
-            mbar_init(bar(B_PVDONE + x), 1);
-        }
-        for (int s = 0; s < NST; ++s) {
-            mbar_init(bar(B_KFULL + s), 1);
-            mbar_init(bar(B_KEMPTY + s), 1);
-            mbar_init(bar(B_VFULL + s), 1);
-            mbar_init(bar(B_VEMPTY + s), 1);
-        }
-        *abort_flag = 0;
-        *err_sh = 0;
-        fence_mbar_init();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tmem_slot;
     const uint64_t lim = p.timeout_ns, drain = p.drain_ns;
-    Walk<ROWS> seg(p, w0, w1, (int)plan[1], plan[0]);
+    if (w0 < w1) {
+    Walk<ROWS> seg(p, w0, w1, (int)plan[1], plan[0], *plan_seq);
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             int used = 0, segs = 0;   // key blocks and segments so far
-            int issued_k[NST] = {}, issued_v[NST] = {}, issued_q = 0;
-            const uint32_t qbytes = 2u * 128u * (uint32_t)(p.group * p.tile_nodes);
+            int issued_k[NST] = {}, issued_v[NST] = {}, issued_q[2] = {};
+            const uint32_t qbytes = 2u * 128u * (uint32_t)(p.group * p.box_nodes);
             bool ok = true;
             for (; ok && seg.next(); ++segs) {
-                const int tiles = ROWS ? min(2, seg.s.tiles - 2 * seg.it) : 1;
-                if (segs && !mbar_wait(bar(B_QEMPTY), (segs - 1) & 1, lim, abort_flag)) { fail(81); break; }
-                mbar_arrive_expect_tx(bar(B_QFULL), tiles * qbytes);
+                const int tiles = seg.tiles(), qb = segs % p.q_bufs;
+                if (segs >= p.q_bufs && !wait_phase(bar(B_QEMPTY + qb), (segs / p.q_bufs - 1) & 1, lim, abort_flag)) { fail(81); break; }
+                mbar_arrive_expect_tx(bar(B_QFULL + qb), tiles * qbytes);
                 for (int x = 0; x < tiles; ++x) {
                     const int row = (int)(seg.s.bos + (ROWS ? 2 * seg.it + x : 0) * p.tile_nodes);
-                    tma_load_3d(smem_u32(sm + C::kQ + x * kBlk), &mQ, 0, seg.h * p.group, row, bar(B_QFULL));
-                    tma_load_3d(smem_u32(sm + C::kQ + x * kBlk + kHalf), &mQ, 64, seg.h * p.group, row, bar(B_QFULL));
+                    const uint32_t at = smem_u32(sm + C::kQ + x * kBlk) + qb * (kHalf / 2);
+                    tma_load_3d(at, &mQ, 0, seg.h * p.group, row, bar(B_QFULL + qb));
+                    tma_load_3d(at + kHalf, &mQ, 64, seg.h * p.group, row, bar(B_QFULL + qb));
                 }
-                ++issued_q;
+                ++issued_q[qb];
                 for (int j = seg.blk0; j < seg.blk1; ++j, ++used) {
                     const int s = used % NST;
                     const uint32_t ph = ((used - NST) / NST) & 1;
@@ -275,154 +362,137 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_3d(smem_u32(sm + at + kHalf), cache, 64, seg.h, row, full);
                         }
                     };
-                    if (used >= NST && !mbar_wait(bar(B_KEMPTY + s), ph, lim, abort_flag)) { fail(82); ok = false; break; }
+                    if (used >= NST && !wait_phase(bar(B_KEMPTY + s), ph, lim, abort_flag)) { fail(82); ok = false; break; }
                     copy(C::kK + s * kBlk, &mKc, &mKn, bar(B_KFULL + s));
                     ++issued_k[s];
-                    if (used >= NST && !mbar_wait(bar(B_VEMPTY + s), ph, lim, abort_flag)) { fail(83); ok = false; break; }
+                    if (used >= NST && !wait_phase(bar(B_VEMPTY + s), ph, lim, abort_flag)) { fail(83); ok = false; break; }
                     copy(C::kV + s * kBlk, &mVc, &mVn, bar(B_VFULL + s));
                     ++issued_v[s];
                 }
             }
             const int zero = 0;   // no copy may still be landing in shared memory at exit
-            if (issued_q) mbar_wait(bar(B_QFULL), (issued_q - 1) & 1, drain, &zero);
+            for (int s = 0; s < 2; ++s)
+                if (issued_q[s]) wait_phase(bar(B_QFULL + s), (issued_q[s] - 1) & 1, drain, &zero);
             for (int s = 0; s < NST; ++s) {
-                if (issued_k[s]) mbar_wait(bar(B_KFULL + s), (issued_k[s] - 1) & 1, drain, &zero);
-                if (issued_v[s]) mbar_wait(bar(B_VFULL + s), (issued_v[s] - 1) & 1, drain, &zero);
+                if (issued_k[s]) wait_phase(bar(B_KFULL + s), (issued_k[s] - 1) & 1, drain, &zero);
+                if (issued_v[s]) wait_phase(bar(B_VFULL + s), (issued_v[s] - 1) & 1, drain, &zero);
             }
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16(kBM, kBN, false, false);   // Q (K-major) x K (K-major)
-            const uint32_t id_o = idesc_bf16(kBM, kD, false, true);     // P (TMEM) x V (MN-major)
-            const uint64_t dKm = desc_sw128(smem_u32(sm), 16, 1024);
-            const uint64_t dMN = desc_sw128(smem_u32(sm), kHalf, 1024);
-            int used = 0, segs = 0;
-            int pvs[2] = {0, 0}, ps[2] = {0, 0};   // P V products issued, P blocks waited for, per stream
-            // S_x = Q K^T of block `at` (its K already waited for), once P_x V of the block before has read S_x
-            auto qk = [&](int x, int at) -> bool {
-                if (pvs[x] && !mbar_wait(bar(B_PVDONE + x), (pvs[x] - 1) & 1, lim, abort_flag)) { fail(84); return false; }
-                tc_fence_after();
-                const uint32_t kofs = C::kK + (at % NST) * kBlk, qofs = C::kQ + (ROWS ? x * kBlk : 0);
-#pragma unroll
-                for (int ks = 0; ks < kD / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-                    mma_bf16_ss(tm + TM_S + x * kBN, dKm + ((qofs + off) >> 4), dKm + ((kofs + off) >> 4), id_s, ks > 0);
-                }
-                mma_commit(bar(B_SFULL + x));
-                return true;
-            };
-            // O_x (+)= P_x V, over the keys that count (P is zero beyond them)
-            auto pv = [&](int x, int at, int steps, bool first) -> bool {
-                if (!mbar_wait(bar(B_PREADY + x), ps[x]++ & 1, lim, abort_flag)) { fail(85); return false; }
-                if (!mbar_wait(bar(B_VFULL + at % NST), (at / NST) & 1, lim, abort_flag)) { fail(86); return false; }
-                tc_fence_after();
-                const uint32_t vofs = C::kV + (at % NST) * kBlk;
-                for (int ks = 0; ks < steps; ++ks)
-                    mma_bf16_ts(tm + TM_O + x * kD, tm + TM_S + x * kBN + (ks >> 2) * 64 + (ks & 3) * 8,
-                                dMN + ((vofs + ks * 2048) >> 4), id_o, (!first || ks > 0) ? 1u : 0u);
-                mma_commit(bar(B_PVDONE + x));
-                ++pvs[x];
-                return true;
-            };
-            auto k_ready = [&](int at) -> bool {
-                if (mbar_wait(bar(B_KFULL + at % NST), (at / NST) & 1, lim, abort_flag)) return true;
-                fail(87);
-                return false;
-            };
-            bool ok = true;
-            for (; ok && seg.next(); ++segs) {
-                const int nblk = seg.blk1 - seg.blk0;
-                if (!mbar_wait(bar(B_QFULL), segs & 1, lim, abort_flag)) { fail(88); break; }
-                if (ROWS) {
-                    const int tiles = min(2, seg.s.tiles - 2 * seg.it);
-                    // the scores of block jj for stream x; after the last stream the K stage is free
-                    auto scores = [&](int x, int jj) -> bool {
-                        if ((x == 0 && !k_ready(used + jj)) || !qk(x, used + jj)) return false;
-                        if (x == tiles - 1) {
-                            mma_commit(bar(B_KEMPTY + (used + jj) % NST));
-                            if (jj == nblk - 1) mma_commit(bar(B_QEMPTY));
-                        }
-                        return true;
-                    };
-                    for (int x = 0; ok && x < tiles; ++x) ok = scores(x, 0);
-                    for (int jj = 0; ok && jj < nblk; ++jj) {
-                        const int steps = (seg.valid(seg.blk0 + jj) + 15) / 16;
-                        for (int x = 0; ok && x < tiles; ++x) {
-                            ok = pv(x, used + jj, steps, jj == 0);
-                            if (ok && x == tiles - 1) mma_commit(bar(B_VEMPTY + (used + jj) % NST));
-                            if (ok && jj + 1 < nblk) ok = scores(x, jj + 1);
-                        }
-                    }
-                } else {
-                    auto scores = [&](int jj) -> bool {
-                        if (!k_ready(used + jj) || !qk(jj & 1, used + jj)) return false;
-                        mma_commit(bar(B_KEMPTY + (used + jj) % NST));
-                        if (jj == nblk - 1) mma_commit(bar(B_QEMPTY));
-                        return true;
-                    };
-                    ok = scores(0);
-                    if (ok && nblk > 1) ok = scores(1);
-                    for (int jj = 0; ok && jj < nblk; ++jj) {
-                        ok = pv(jj & 1, used + jj, (seg.valid(seg.blk0 + jj) + 15) / 16, jj < 2);
-                        if (ok) mma_commit(bar(B_VEMPTY + (used + jj) % NST));
-                        if (ok && jj + 2 < nblk) ok = scores(jj + 2);
-                    }
-                }
-                used += nblk;
+        constexpr uint32_t id_s = idesc_bf16(kBM, kSub, false, false);  // Q (K-major) x K (K-major)
+        constexpr uint32_t id_o = idesc_bf16(kBM, kD, false, true);     // P (TMEM) x V (MN-major)
+        const uint64_t dKm = desc_sw128(smem_u32(sm), 16, 1024);
+        const uint64_t dMN = desc_sw128(smem_u32(sm), kHalf, 1024);
+        int used = 0, segs = 0;
+        int qks[2] = {0, 0}, pvs[2] = {0, 0};   // score and output products issued, per stream
+        bool ok = true;
+        auto wait = [&](int b, uint32_t parity, int code) {
+            if (!__all_sync(kAll, wait_phase(bar(b), parity, lim, abort_flag))) {
+                fail(code);
+                ok = false;
             }
-            mma_commit(bar(B_FIN));   // every issued MMA completes before TMEM is released
-            const int zero = 0;
-            mbar_wait(bar(B_FIN), 0, drain, &zero);
+            return ok;
+        };
+        for (; ok && seg.next(); ++segs) {
+            const int qb = segs % p.q_bufs;
+            if (!wait(B_QFULL + qb, (segs / p.q_bufs) & 1, 84)) break;
+            // S = Q K^T of half block `a` for all streams that have it, into the
+            // buffer whose P the product before last has read
+            auto scores = [&](const Halves<ROWS> &a) {
+                const int at = used + a.j - seg.blk0, s = at % NST;
+                if (!wait(B_KFULL + s, (at / NST) & 1, 85)) return;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!a.has(seg, x)) continue;
+                    const int n = qks[x];
+                    if (n >= 2 && !wait(B_PVDONE + 2 * x + (n & 1), ((n - 2) >> 1) & 1, 86)) return;
+                    tc_fence_after();
+                    const uint64_t kd = dKm + ((C::kK + s * kBlk + a.half(x) * (kHalf / 2)) >> 4);
+                    const uint64_t qd = dKm + ((C::kQ + (ROWS ? x * kBlk : qb * (kHalf / 2))) >> 4);
+                    const uint32_t d = tm + TM_S + x * 128 + (n & 1) * kSub;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < kD / 16; ++ks) {
+                            const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                            mma_bf16_ss(d, qd + off, kd + off, id_s, ks > 0);
+                        }
+                        mma_commit(bar(B_SFULL + 2 * x + (n & 1)));
+                    }
+                    __syncwarp();
+                    ++qks[x];
+                }
+                if (a.last(seg) && elect_one()) {
+                    mma_commit(bar(B_KEMPTY + s));
+                    if (a.j == seg.blk1 - 1) mma_commit(bar(B_QEMPTY + qb));
+                }
+                __syncwarp();
+            };
+            Halves<ROWS> a{seg.blk0, 0}, c{seg.blk0, 0};   // next scores, next outputs
+            for (int i = 0; ok && i < 2 && !a.done(seg); ++i, a.step(seg)) scores(a);
+            bool first[2] = {true, true};
+            for (; ok && !c.done(seg); c.step(seg)) {
+                const int at = used + c.j - seg.blk0, s = at % NST, valid = seg.valid(c.j);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (!ok || !c.has(seg, x)) continue;
+                    const int n = pvs[x], h = c.half(x);
+                    if (!wait(B_PREADY + 2 * x + (n & 1), (n >> 1) & 1, 87) || !wait(B_VFULL + s, (at / NST) & 1, 88)) continue;
+                    tc_fence_after();
+                    // O (+)= P V, over the keys that count (P is zero beyond them)
+                    const int steps = (min(kSub, valid - kSub * h) + 15) / 16;
+                    const uint64_t vd = dMN + ((C::kV + s * kBlk + h * (kHalf / 2)) >> 4);
+                    const uint32_t pa = tm + TM_S + x * 128 + (n & 1) * kSub;
+                    const uint32_t more = first[x] ? 0u : 1u;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < kSub / 16; ++ks)
+                            if (ks < steps) mma_bf16_ts(tm + TM_O + x * kD, pa + ks * 8, vd + ks * (2048 >> 4), id_o, ks > 0 ? 1u : more);
+                        mma_commit(bar(B_PVDONE + 2 * x + (n & 1)));
+                    }
+                    __syncwarp();
+                    first[x] = false;
+                    ++pvs[x];
+                }
+                if (ok && c.last(seg) && elect_one()) mma_commit(bar(B_VEMPTY + s));
+                __syncwarp();
+                if (ok && !a.done(seg)) {
+                    scores(a);
+                    a.step(seg);
+                }
+            }
+            used += seg.blk1 - seg.blk0;
         }
+        if (elect_one()) mma_commit(bar(B_FIN));   // every issued MMA completes before TMEM is released
+        __syncwarp();
+        const int zero = 0;
+        wait_phase(bar(B_FIN), 0, drain, &zero);
     } else {
-        // ------------------------------------------------------------ softmax (warps 0-15)
+        // ------------------------------------------------------------ softmax (warps 0-7)
         // A wait that gives up does not leave the loops (others could be
         // waiting at an exchange): with the abort flag set the remaining waits
         // return at once and nothing is stored.
-        const int x = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1, gtid = tid & 255;
-        const int r = 32 * quarter + lane;
-        const uint32_t lane_off = static_cast<uint32_t>(32 * quarter) << 16;
-        const uint32_t sa = tm + lane_off + TM_S + x * kBN + 64 * half;
-        const uint32_t oa = tm + lane_off + TM_O + x * kD + 64 * half;
+        const int x = warp >> 2, gtid = tid & 127;
+        const int r = gtid;                      // row of the tile = TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t oa = tm + lane_off + TM_O + x * kD;
         const float c = p.c;
-        float *xch = reinterpret_cast<float *>(ctl + kOffXch);            // [stream][128 rows][2]
-        float *mine = xch + (x * 128 + r) * 2 + half, *other = xch + (x * 128 + r) * 2 + (half ^ 1);
+        float2 *xch = reinterpret_cast<float2 *>(ctl + kOffXch);          // [stream][128 rows]
         int8_t *par = reinterpret_cast<int8_t *>(ctl + kOffPar) + x * 64;
-        const int bar_pair = 1 + 4 * x + quarter, bar_group = 9 + x, bar_both = 11;
-        // the sum of the halves' values of this row
-        auto pair_sum = [&](float v) -> float {
-            named_bar_sync(bar_pair, 64);
-            *mine = v;
-            named_bar_sync(bar_pair, 64);
-            return v + *other;
-        };
-        // the larger of the halves' values as bf16: m only has to be the same in
-        // both halves and within a factor of the maximum (two parities keep
-        // consecutive exchanges apart)
-        __nv_bfloat16 *mx_sh = reinterpret_cast<__nv_bfloat16 *>(xch) + (x * 128 + r) * 4;   // [2 parities][2 halves]
-        int parity = 0;
-        auto pair_max = [&](float v) -> float {
-            const __nv_bfloat16 w = __float2bfloat16_rn(v);
-            __nv_bfloat16 *at = mx_sh + 2 * parity;
-            parity ^= 1;
-            at[half] = w;
-            named_bar_sync(bar_pair, 64);
-            return fmaxf(__bfloat162float(w), __bfloat162float(at[half ^ 1]));
-        };
-        int used = 0, cnt = 0;                   // key blocks so far; blocks of this stream so far
+        const int bar_group = 1 + x, bar_both = 3;
+        int used = 0, cnt = 0;                   // key blocks so far; half blocks of this stream so far
         bool ok = true;
         auto wait = [&](int b, uint32_t parity, int code) {
-            if (!__all_sync(kAll, mbar_wait(bar(b), parity, lim, abort_flag))) {
+            if (!__all_sync(kAll, wait_phase(bar(b), parity, lim, abort_flag))) {
                 fail(code);
                 ok = false;
             }
         };
+        auto wait_pv = [&](int n, int code) { wait(B_PVDONE + 2 * x + (n & 1), (n >> 1) & 1, code); };   // P V of half block n
         while (seg.next()) {
-            const int nblk = seg.blk1 - seg.blk0;
             const int tile = ROWS ? 2 * seg.it + x : 0;
             if (ROWS && tile >= seg.s.tiles) {   // an odd tile count leaves stream 1 without rows
-                used += nblk;
+                used += seg.blk1 - seg.blk0;
                 continue;
             }
             const int node = tile * p.tile_nodes + r / p.group;
@@ -433,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int depth = 0;
             const bool need_tree = seg.draft(seg.blk1 - 1) || p.window;
             if (need_tree && p.parents) {
-                named_bar_sync(bar_group, 256);
+                named_bar_sync(bar_group, 128);
                 if (gtid < seg.s.n) par[gtid] = (int8_t)tree_parent(p.parents, seg.s.bos, gtid);
-                named_bar_sync(bar_group, 256);
+                named_bar_sync(bar_group, 128);
             }
             if (need_tree && vrow) {
                 if (p.parents) {
@@ -454,27 +524,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             // only keys at positions above `far` are inside the window
             const int32_t *pos = p.window && p.pos ? p.pos + ((int64_t)seg.b * p.Hkv + seg.h) * p.capacity : nullptr;
             const int far = p.window ? (pos ? p.seen[seg.b] : seg.s.len) + depth - p.window : INT32_MIN;
-            // positions of this half's keys, two a lane, fetched a block ahead
+            const int top = p.window ? __reduce_max_sync(kAll, vrow ? far : INT32_MIN) : 0;   // the warp's last masked position
+            Halves<ROWS> a{seg.blk0, 0};
+            while (!a.done(seg) && !a.has(seg, x)) a.step(seg);   // by keys, short blocks have nothing for stream 1
+            // positions of a half block's keys, two a lane, fetched ahead
             int p0 = INT32_MAX, p1 = INT32_MAX;
-            auto fetch_pos = [&](int jj) {
+            auto fetch_pos = [&](const Halves<ROWS> &f) {
                 p0 = p1 = INT32_MAX;
-                if (!pos || !work || jj >= nblk || seg.draft(seg.blk0 + jj)) return;
-                const int k0 = seg.key0(seg.blk0 + jj) + 64 * half;
+                if (!work || f.done(seg) || seg.draft(f.j)) return;
+                const int k0 = seg.key0(f.j) + kSub * f.half(x);
                 if (k0 + lane < seg.s.len) p0 = pos[k0 + lane];
                 if (k0 + 32 + lane < seg.s.len) p1 = pos[k0 + 32 + lane];
             };
-            fetch_pos(ROWS ? 0 : x);
-            const int top = p.window ? __reduce_max_sync(kAll, vrow ? far : INT32_MIN) : 0;   // the warp's last masked position
-            float m = -INFINITY, l = 0.f;   // m: the same in both halves of a row; l: this half's share
-            for (int jj = ROWS ? 0 : x; jj < nblk; jj += ROWS ? 1 : 2) {
-                const int j = seg.blk0 + jj, valid = seg.valid(j);
-                const bool draft = seg.draft(j);
-                uint64_t vis;                // which of this half's 64 keys the row sees
-                if (draft) {
-                    vis = half ? 0 : anc;
+            if (pos) fetch_pos(a);
+            float m = -INFINITY, l = 0.f;
+            const int cnt0 = cnt;
+            while (!a.done(seg)) {
+                const int j = a.j, h = a.half(x), valid = seg.valid(j) - kSub * h;   // keys of this half, 64 at most counting
+                uint64_t vis;                    // which of them the row sees
+                if (seg.draft(j)) {
+                    vis = anc;
                 } else {
-                    const int left = valid - 64 * half, k0 = seg.key0(j) + 64 * half;
-                    vis = left >= 64 ? ~0ull : left <= 0 ? 0 : (1ull << left) - 1;
+                    const int k0 = seg.key0(j) + kSub * h;
+                    vis = valid >= kSub ? ~0ull : (1ull << valid) - 1;
                     if (p.window && work) {
                         if (pos) {
                             if (__reduce_min_sync(kAll, min(p0, p1)) <= top) {
@@ -487,34 +559,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         } else if (k0 <= top) {
                             const int skip = far + 1 - k0;   // keys of this half before the window
-                            if (skip > 0) vis &= skip >= 64 ? 0 : ~0ull << skip;
+                            if (skip > 0) vis &= skip >= kSub ? 0 : ~0ull << skip;
                         }
                     }
                 }
-                if (pos) fetch_pos(jj + (ROWS ? 1 : 2));
-                wait(B_SFULL + x, cnt & 1, 89);
-                ++cnt;
+                const int at = used + j - seg.blk0;
+                Halves<ROWS> f = a;
+                do f.step(seg);
+                while (!f.done(seg) && !f.has(seg, x));
+                if (pos) fetch_pos(f);
+                a = f;
+                const int buf = cnt & 1;
+                const uint32_t sa = tm + lane_off + TM_S + x * 128 + buf * kSub;
+                wait(B_SFULL + 2 * x + buf, (cnt >> 1) & 1, 89);
                 tc_fence_after();
                 if (work) {
-                    const bool masked = !__all_sync(kAll, vis == ~0ull);
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c4 = 0; c4 < 2; ++c4) {
-                        float v[32];
-                        tmem_ld32(sa + 32 * c4, v);
-                        float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        if (masked) {
-                            const uint32_t bits = (uint32_t)(vis >> (32 * c4));
+                    float v[64];
+                    tmem_ld64(sa, v);
+                    if (!__all_sync(kAll, vis == ~0ull)) {
+                        const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (bits >> i & 1) a[i & 3] = fmaxf(a[i & 3], v[i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) a[i & 3] = fmaxf(a[i & 3], v[i]);
+                        for (int i = 0; i < 32; ++i) {
+                            if (!(lo >> i & 1)) v[i] = -INFINITY;
+                            if (!(hi >> i & 1)) v[32 + i] = -INFINITY;
                         }
-                        mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
                     }
-                    const float mb = pair_max(mx) * c;
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+                    const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                     float alpha = 1.f;
                     bool rescale = false;
                     if (mb > m + kRescaleThreshold) {   // also taken when m is still -inf
@@ -525,55 +598,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = mb;
                     }
                     const float msub = m == -INFINITY ? 0.f : m;
-                    float sum = 0.f;
-#pragma unroll 1
-                    for (int c4 = 0; c4 < 2; ++c4) {
-                        float v[32];
-                        tmem_ld32(sa + 32 * c4, v);
-                        uint32_t pk[16];
-                        float sm4[4] = {0.f, 0.f, 0.f, 0.f};
-                        const uint32_t bits = (uint32_t)(vis >> (32 * c4));
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t pk[32];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float p0 = ex2_approx(fmaf(v[i], c, -msub)), p1 = ex2_approx(fmaf(v[i + 1], c, -msub));
-                            if (masked) {
-                                if (!(bits >> i & 1)) p0 = 0.f;
-                                if (!(bits >> (i + 1) & 1)) p1 = 0.f;
-                            }
-                            sm4[(i >> 1) & 3] += p0 + p1;
-                            pk[i >> 1] = pack_bf16(p0, p1);
-                        }
-                        tmem_st16u(sa + 16 * c4, pk);   // over columns read by now
-                        sum += (sm4[0] + sm4[1]) + (sm4[2] + sm4[3]);
+                    for (int i = 0; i < 64; i += 2) {
+                        const float e0 = ex2_approx(fmaf(v[i], c, -msub)), e1 = ex2_approx(fmaf(v[i + 1], c, -msub));
+                        sum[(i >> 1) & 3] += e0 + e1;
+                        pk[i >> 1] = pack_bf16(e0, e1);
                     }
-                    l = l * alpha + sum;
-                    if (__any_sync(kAll, rescale)) {    // O_x is stable: P_x V of the block before has completed
+                    tmem_st32u(sa, pk);
+                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    if (__any_sync(kAll, rescale)) {    // once P V of the half block before has completed
+                        if (cnt > cnt0) wait_pv(cnt - 1, 90);
+                        tc_fence_after();
 #pragma unroll 1
-                        for (int c4 = 0; c4 < 2; ++c4) {
-                            float v[32];
-                            tmem_ld32(oa + 32 * c4, v);
+                        for (int c4 = 0; c4 < 4; ++c4) {
+                            float o[32];
+                            tmem_ld32(oa + 32 * c4, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                            tmem_st32(oa + 32 * c4, v);
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tmem_st32(oa + 32 * c4, o);
                         }
                     }
                 }
                 // V rows behind the last key, up to the 16 of a product step, may hold
                 // anything; P is zero there and the rows are cleared
-                const int behind = (16 - valid % 16) % 16;
+                const int behind = valid < kSub ? (16 - valid % 16) % 16 : 0;
                 if (behind && (!ROWS || x == 0)) {
-                    const int at = used + jj, s = at % NST;
-                    wait(B_VFULL + s, (at / NST) & 1, 90);
-                    if (gtid < behind * 16) {
-                        const int row = valid + gtid / 16, ch = gtid % 16;
+                    const int s = at % NST;
+                    wait(B_VFULL + s, (at / NST) & 1, 91);
+                    for (int e = gtid; e < behind * 16; e += 128) {
+                        const int row = kSub * h + valid + e / 16, ch = e % 16;
                         st_shared_v4(smem_u32(sm + C::kV + s * kBlk + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16), 0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
+                ++cnt;
                 tc_fence_before();
-                mbar_arrive(bar(B_PREADY + x));
+                mbar_arrive(bar(B_PREADY + 2 * x + buf));
             }
-            used += nblk;
+            used += seg.blk1 - seg.blk0;
             const bool whole = seg.blk0 == 0 && seg.blk1 == seg.s.blocks;
             // an item that began in an earlier CTA goes to slot 2c, one that goes on into the next to 2c + 1
             const int slot = 2 * cta + (seg.blk0 > 0 ? 0 : 1);
@@ -601,56 +665,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p.ml[part_at] = make_float2(mm, ll);
                 }
             };
+            if (cnt > cnt0) wait_pv(cnt - 1, 92);
             if (ROWS) {
-                wait(B_PVDONE + x, (cnt - 1) & 1, 91);
                 tc_fence_after();
                 if (work) {
-                    const float lsum = pair_sum(l);
-                    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
-                    for (int c4 = 0; c4 < 2; ++c4) {
+                    for (int c4 = 0; c4 < 4; ++c4) {
                         float v[32];
                         tmem_ld32(oa + 32 * c4, v);
-                        if (vrow && ok) store(64 * half + 32 * c4, v, inv);
+                        if (vrow && ok) store(32 * c4, v, inv);
                     }
-                    if (vrow && ok && half == 0) store_ml(m, lsum);
+                    if (vrow && ok) store_ml(m, l);
                 }
             } else {
-                // merge the streams: each takes 32 of the half's 64 columns
-                const bool two = nblk > 1;
-                if (x == 0 || two) wait(B_PVDONE + x, (cnt - 1) & 1, 92);
-                const float lrow = work ? pair_sum(l) : 0.f;   // a stream without blocks: m = -inf, l = 0
+                // merge the streams; each writes 64 columns
+                xch[x * 128 + r] = make_float2(m, l);             // a stream without keys: m = -inf, l = 0
                 tc_fence_before();
                 named_bar_sync(bar_both, 32 * kSoftmaxWarps);     // both streams' products have completed
                 tc_fence_after();
-                if (half == 0) *mine = m;
-                else *mine = lrow;
-                named_bar_sync(bar_both, 32 * kSoftmaxWarps);
                 if (work) {
-                    const float m0 = xch[2 * r], l0 = xch[2 * r + 1], m1 = xch[256 + 2 * r], l1 = xch[257 + 2 * r];
-                    const float mm = fmaxf(m0, m1);
-                    const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
-                    const float ll = f0 * l0 + f1 * l1, inv = ll > 0.f ? 1.f / ll : 0.f;
-                    const uint32_t at = tm + lane_off + TM_O + 64 * half + 32 * x;
-                    float v[32];
-                    tmem_ld32(at, v);
+                    const float2 s0 = xch[r], s1 = xch[128 + r];
+                    const float mm = fmaxf(s0.x, s1.x);
+                    const float f0 = s0.x == -INFINITY ? 0.f : ex2_approx(s0.x - mm), f1 = s1.x == -INFINITY ? 0.f : ex2_approx(s1.x - mm);
+                    const float ll = f0 * s0.y + f1 * s1.y, inv = ll > 0.f ? 1.f / ll : 0.f;
+                    // a stream that had no half block in this segment has no accumulator
+                    const bool two = seg.valid(seg.blk0) > kSub;   // full blocks come first
+#pragma unroll 1
+                    for (int c4 = 0; c4 < 2; ++c4) {
+                        float v[32];
+                        tmem_ld32(tm + lane_off + TM_O + 64 * x + 32 * c4, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= f0;
-                    if (two) {
-                        float u[32];
-                        tmem_ld32(at + kD, u);
+                        for (int i = 0; i < 32; ++i) v[i] *= f0;
+                        if (two) {
+                            float u[32];
+                            tmem_ld32(tm + lane_off + TM_O + kD + 64 * x + 32 * c4, u);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = fmaf(u[i], f1, v[i]);
+                            for (int i = 0; i < 32; ++i) v[i] = fmaf(u[i], f1, v[i]);
+                        }
+                        if (vrow && ok) store(64 * x + 32 * c4, v, inv);
                     }
-                    if (vrow && ok) {
-                        store(64 * half + 32 * x, v, inv);
-                        if (half == 0 && x == 0) store_ml(mm, ll);
-                    }
+                    if (vrow && ok && x == 0) store_ml(mm, ll);
                 }
                 tc_fence_before();
                 named_bar_sync(bar_both, 32 * kSoftmaxWarps);   // both accumulators read, the exchange free
             }
         }
+    }
     }
     tc_fence_before();
     __syncthreads();
@@ -696,7 +757,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const Params
         const int tile = (int)node / p.tile_nodes, it = ROWS ? tile / 2 : tile;
         const int r = (ROWS ? (tile & 1) * kBM : 0) + ((int)node % p.tile_nodes) * p.group + hq % p.group;
         const int64_t W = p.prefix[p.num_seqs], runs = min((int64_t)ctas, W);
-        const int64_t start = p.prefix[b] + ((int64_t)h * s.items + it) * s.blocks, last = start + s.blocks - 1;
+        const int64_t start = p.prefix[b] + ((int64_t)h * s.items + it) * s.cost() + kItemCost, last = start + s.blocks - 1;
         const int c0 = (int)(((start + 1) * runs - 1) / W), c1 = (int)(((last + 1) * runs - 1) / W);
         split = c1 > c0;
         if (split) {
@@ -788,9 +849,12 @@ template <bool ROWS> cudaError_t launch(const TreeAttnLaunch &L, cudaStream_t st
     p.ml = reinterpret_cast<float2 *>(ws + w.ml);
     p.part = reinterpret_cast<float *>(ws + w.part);
     p.timeout_ns = L.timeout_ns; p.drain_ns = L.drain_ns;
+    // trees of at most half a tile leave room for the next item's Q beside this one's
+    p.box_nodes = ROWS ? nodes : L.max_nodes;
+    p.q_bufs = !ROWS && group * L.max_nodes <= kBM / 2 ? 2 : 1;
     CUtensorMap mq, mkc, mvc, mkn, mvn;
     const int64_t rows = (int64_t)L.num_seqs * L.capacity;
-    bool ok = make_rows_map(&mq, L.q, L.total_nodes, L.Hq, group, nodes) && make_rows_map(&mkn, L.k, L.total_nodes, L.Hkv, 1, kBox) &&
+    bool ok = make_rows_map(&mq, L.q, L.total_nodes, L.Hq, group, p.box_nodes) && make_rows_map(&mkn, L.k, L.total_nodes, L.Hkv, 1, kBox) &&
               make_rows_map(&mvn, L.v, L.total_nodes, L.Hkv, 1, kBox);
     if (ok && rows > 0) {
         ok = make_rows_map(&mkc, L.k_cache, rows, L.Hkv, 1, kBN) && make_rows_map(&mvc, L.v_cache, rows, L.Hkv, 1, kBN);

@@ -175,7 +175,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)   # current_stream(device).cuda_stream without the object
 
 
 def gdn_prefill_workspace_size(num_seqs: int, total_tokens: int, H: int, dk: int, dv: int,
