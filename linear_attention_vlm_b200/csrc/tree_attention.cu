@@ -27,7 +27,9 @@
 // 64 scores in registers, so a row needs no exchange and its scores are read once.
 //   warps 0-3 / 4-7   softmax of stream 0 / 1 (a thread per row)
 //   warp 8            TMA producer: Q per item, K and V through rings
-//   warp 9            MMA issuer (one lane)
+//   warps 9, 10       MMA issuers of stream 0 / 1: with one warp for both, its
+//                     waits and issues (about 3000 cycles per half block) were
+//                     longer than the products and the softmax (1200 each)
 // Tensor memory: per stream 2 x 64 columns of scores and 128 of output; the bf16
 // P of a half block lies over the columns of its S, read by then.
 #include <cuda.h>
@@ -53,7 +55,7 @@ constexpr float kRescaleThreshold = 8.f;   // log2 units, as in the window atten
 constexpr int kMaxCtas = 160;
 
 constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 32 * 10;
+constexpr int kThreads = 32 * 11;
 constexpr int kSub = 64;                // keys of a half block
 // Planning weight of an item beside its key blocks: starting one (its Q, the
 // first scores) and ending it (merge and stores) take about a block's time.
@@ -233,19 +235,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 32 * kProducerWarp) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_QFULL + i), 1);
-            mbar_init(bar(B_QEMPTY + i), 1);
+            mbar_init(bar(B_QEMPTY + i), 2);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(B_PVDONE + i), 1);
             mbar_init(bar(B_SFULL + i), 1);
             mbar_init(bar(B_PREADY + i), 32 * kSoftmaxWarps / 2);
         }
-        mbar_init(bar(B_FIN), 1);
+        mbar_init(bar(B_FIN), 2);
         for (int s = 0; s < NST; ++s) {
             mbar_init(bar(B_KFULL + s), 1);
-            mbar_init(bar(B_KEMPTY + s), 1);
+            mbar_init(bar(B_KEMPTY + s), 2);
             mbar_init(bar(B_VFULL + s), 1);
-            mbar_init(bar(B_VEMPTY + s), 1);
+            mbar_init(bar(B_VEMPTY + s), 2);
         }
         *abort_flag = 0;
         *err_sh = 0;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // total units, then the sequence that this CTA's run starts in
     int64_t *plan = reinterpret_cast<int64_t *>(ctl + kOffPlan);                // units before the first sequence, its index
     Seq *plan_seq = reinterpret_cast<Seq *>(plan + 2);
-    int64_t *wsum = reinterpret_cast<int64_t *>(sm);                            // [10] scratch before any copy lands
+    int64_t *wsum = reinterpret_cast<int64_t *>(sm);                            // [11] scratch before any copy lands
     static_assert(16 + sizeof(Seq) <= kOffPar - kOffPlan, "plan area");
     int64_t W = 0, w0 = 0, w1 = 0;
     const bool one_pass = p.num_seqs <= kThreads;
@@ -378,14 +380,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (issued_v[s]) wait_phase(bar(B_VFULL + s), (issued_v[s] - 1) & 1, drain, &zero);
             }
         }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issuer
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuers, one warp per stream
+        // Both release every stage, whether they had a product on it or not.
+        const int x = warp - kMmaWarp;
         constexpr uint32_t id_s = idesc_bf16(kBM, kSub, false, false);  // Q (K-major) x K (K-major)
         constexpr uint32_t id_o = idesc_bf16(kBM, kD, false, true);     // P (TMEM) x V (MN-major)
         const uint64_t dKm = desc_sw128(smem_u32(sm), 16, 1024);
         const uint64_t dMN = desc_sw128(smem_u32(sm), kHalf, 1024);
         int used = 0, segs = 0;
-        int qks[2] = {0, 0}, pvs[2] = {0, 0};   // score and output products issued, per stream
+        int qks = 0, pvs = 0;   // score and output products issued
         bool ok = true;
         auto wait = [&](int b, uint32_t parity, int code) {
             if (!__all_sync(kAll, wait_phase(bar(b), parity, lim, abort_flag))) {
@@ -397,19 +401,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; ok && seg.next(); ++segs) {
             const int qb = segs % p.q_bufs;
             if (!wait(B_QFULL + qb, (segs / p.q_bufs) & 1, 84)) break;
-            // S = Q K^T of half block `a` for all streams that have it, into the
-            // buffer whose P the product before last has read
+            const uint64_t qd = dKm + ((C::kQ + (ROWS ? x * kBlk : qb * (kHalf / 2))) >> 4);
+            // S = Q K^T of half block `a`, into the buffer whose P the product
+            // before last has read
             auto scores = [&](const Halves<ROWS> &a) {
                 const int at = used + a.j - seg.blk0, s = at % NST;
-                if (!wait(B_KFULL + s, (at / NST) & 1, 85)) return;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (!a.has(seg, x)) continue;
-                    const int n = qks[x];
+                if (a.h == 0 && !wait(B_KFULL + s, (at / NST) & 1, 85)) return;
+                if (a.has(seg, x)) {
+                    const int n = qks;
                     if (n >= 2 && !wait(B_PVDONE + 2 * x + (n & 1), ((n - 2) >> 1) & 1, 86)) return;
                     tc_fence_after();
                     const uint64_t kd = dKm + ((C::kK + s * kBlk + a.half(x) * (kHalf / 2)) >> 4);
-                    const uint64_t qd = dKm + ((C::kQ + (ROWS ? x * kBlk : qb * (kHalf / 2))) >> 4);
                     const uint32_t d = tm + TM_S + x * 128 + (n & 1) * kSub;
                     if (elect_one()) {
 #pragma unroll
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_commit(bar(B_SFULL + 2 * x + (n & 1)));
                     }
                     __syncwarp();
-                    ++qks[x];
+                    ++qks;
                 }
                 if (a.last(seg) && elect_one()) {
                     mma_commit(bar(B_KEMPTY + s));
@@ -430,20 +432,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             Halves<ROWS> a{seg.blk0, 0}, c{seg.blk0, 0};   // next scores, next outputs
             for (int i = 0; ok && i < 2 && !a.done(seg); ++i, a.step(seg)) scores(a);
-            bool first[2] = {true, true};
+            uint32_t more = 0;
             for (; ok && !c.done(seg); c.step(seg)) {
-                const int at = used + c.j - seg.blk0, s = at % NST, valid = seg.valid(c.j);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (!ok || !c.has(seg, x)) continue;
-                    const int n = pvs[x], h = c.half(x);
-                    if (!wait(B_PREADY + 2 * x + (n & 1), (n >> 1) & 1, 87) || !wait(B_VFULL + s, (at / NST) & 1, 88)) continue;
+                const int at = used + c.j - seg.blk0, s = at % NST, h = c.half(x);
+                if (c.h == 0 && !wait(B_VFULL + s, (at / NST) & 1, 88)) break;
+                if (c.has(seg, x)) {
+                    const int n = pvs;
+                    if (!wait(B_PREADY + 2 * x + (n & 1), (n >> 1) & 1, 87)) break;
                     tc_fence_after();
                     // O (+)= P V, over the keys that count (P is zero beyond them)
-                    const int steps = (min(kSub, valid - kSub * h) + 15) / 16;
+                    const int steps = (min(kSub, seg.valid(c.j) - kSub * h) + 15) / 16;
                     const uint64_t vd = dMN + ((C::kV + s * kBlk + h * (kHalf / 2)) >> 4);
                     const uint32_t pa = tm + TM_S + x * 128 + (n & 1) * kSub;
-                    const uint32_t more = first[x] ? 0u : 1u;
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < kSub / 16; ++ks)
@@ -451,12 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_commit(bar(B_PVDONE + 2 * x + (n & 1)));
                     }
                     __syncwarp();
-                    first[x] = false;
-                    ++pvs[x];
+                    more = 1;
+                    ++pvs;
                 }
-                if (ok && c.last(seg) && elect_one()) mma_commit(bar(B_VEMPTY + s));
+                if (c.last(seg) && elect_one()) mma_commit(bar(B_VEMPTY + s));
                 __syncwarp();
-                if (ok && !a.done(seg)) {
+                if (!a.done(seg)) {
                     scores(a);
                     a.step(seg);
                 }
@@ -622,9 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // V rows behind the last key, up to the 16 of a product step, may hold
-                // anything; P is zero there and the rows are cleared
+                // anything; P is zero there and the rows are cleared (by rows both
+                // streams write the same zeros, each before its own product)
                 const int behind = valid < kSub ? (16 - valid % 16) % 16 : 0;
-                if (behind && (!ROWS || x == 0)) {
+                if (behind) {
                     const int s = at % NST;
                     wait(B_VFULL + s, (at / NST) & 1, 91);
                     for (int e = gtid; e < behind * 16; e += 128) {
