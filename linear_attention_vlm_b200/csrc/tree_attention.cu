@@ -106,6 +106,26 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
     for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t d, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 struct Params {
     __nv_bfloat16 *o;
     float *lse;
@@ -525,50 +545,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t *pos = p.window && p.pos ? p.pos + ((int64_t)seg.b * p.Hkv + seg.h) * p.capacity : nullptr;
             const int far = p.window ? (pos ? p.seen[seg.b] : seg.s.len) + depth - p.window : INT32_MIN;
             const int top = p.window ? __reduce_max_sync(kAll, vrow ? far : INT32_MIN) : 0;   // the warp's last masked position
-            Halves<ROWS> a{seg.blk0, 0};
-            while (!a.done(seg) && !a.has(seg, x)) a.step(seg);   // by keys, short blocks have nothing for stream 1
+            // half blocks with all 64 keys, which come first, need no care; the last
+            // block of the cache and the tree's own go through `a`
+            const int full = min(seg.blk1 - seg.blk0, max(0, (seg.s.len - seg.s.kstart) / kBN - seg.blk0));
+            const int plain = ROWS ? 2 * full : full;
+            Halves<ROWS> a{seg.blk0 + full, 0};
+            int k0 = seg.key0(seg.blk0) + (ROWS ? 0 : kSub * x);   // first slot of the half block
+            constexpr int kStep = ROWS ? kSub : kBN;
             // positions of a half block's keys, two a lane, fetched ahead
             int p0 = INT32_MAX, p1 = INT32_MAX;
-            auto fetch_pos = [&](const Halves<ROWS> &f) {
-                p0 = p1 = INT32_MAX;
-                if (!work || f.done(seg) || seg.draft(f.j)) return;
-                const int k0 = seg.key0(f.j) + kSub * f.half(x);
-                if (k0 + lane < seg.s.len) p0 = pos[k0 + lane];
-                if (k0 + 32 + lane < seg.s.len) p1 = pos[k0 + 32 + lane];
+            auto fetch_pos = [&](int k) {
+                p0 = k + lane < seg.s.len ? pos[k + lane] : INT32_MAX;
+                p1 = k + 32 + lane < seg.s.len ? pos[k + 32 + lane] : INT32_MAX;
             };
-            if (pos) fetch_pos(a);
+            const bool by_pos = pos && work;
+            if (by_pos) fetch_pos(k0);
             float m = -INFINITY, l = 0.f;
             const int cnt0 = cnt;
-            while (!a.done(seg)) {
-                const int j = a.j, h = a.half(x), valid = seg.valid(j) - kSub * h;   // keys of this half, 64 at most counting
-                uint64_t vis;                    // which of them the row sees
-                if (seg.draft(j)) {
-                    vis = anc;
-                } else {
-                    const int k0 = seg.key0(j) + kSub * h;
-                    vis = valid >= kSub ? ~0ull : (1ull << valid) - 1;
-                    if (p.window && work) {
-                        if (pos) {
-                            if (__reduce_min_sync(kAll, min(p0, p1)) <= top) {
-                                uint32_t lo = 0, hi = 0;
-                                for (int i = 0; i < 32; ++i) {
-                                    if (__shfl_sync(kAll, p0, i) > far) lo |= 1u << i;
-                                    if (__shfl_sync(kAll, p1, i) > far) hi |= 1u << i;
-                                }
-                                vis &= (uint64_t)hi << 32 | lo;
+            for (int u = 0;; ++u, k0 += kStep) {
+                const bool special = u >= plain;
+                bool masked = false;
+                uint64_t vis = ~0ull;            // which of the 64 keys the row sees
+                int valid = kSub, j = 0, h = 0;
+                if (special) {
+                    while (!a.done(seg) && !a.has(seg, x)) a.step(seg);   // by keys, short blocks have nothing for stream 1
+                    if (a.done(seg)) break;
+                    j = a.j;
+                    h = a.half(x);
+                    valid = min(kSub, seg.valid(j) - kSub * h);
+                    vis = seg.draft(j) ? anc : valid >= kSub ? ~0ull : (1ull << valid) - 1;
+                    masked = true;
+                }
+                if (p.window && work && !(special && seg.draft(j))) {
+                    if (pos) {
+                        if (__reduce_min_sync(kAll, min(p0, p1)) <= top) {
+                            uint32_t lo = 0, hi = 0;
+                            for (int i = 0; i < 32; ++i) {
+                                if (__shfl_sync(kAll, p0, i) > far) lo |= 1u << i;
+                                if (__shfl_sync(kAll, p1, i) > far) hi |= 1u << i;
                             }
-                        } else if (k0 <= top) {
-                            const int skip = far + 1 - k0;   // keys of this half before the window
-                            if (skip > 0) vis &= skip >= kSub ? 0 : ~0ull << skip;
+                            vis &= (uint64_t)hi << 32 | lo;
+                            masked = true;
                         }
+                    } else if (k0 <= top) {
+                        const int skip = far + 1 - k0;   // keys of this half before the window
+                        if (skip > 0) vis &= skip >= kSub ? 0 : ~0ull << skip;
+                        masked = true;
                     }
                 }
-                const int at = used + j - seg.blk0;
-                Halves<ROWS> f = a;
-                do f.step(seg);
-                while (!f.done(seg) && !f.has(seg, x));
-                if (pos) fetch_pos(f);
-                a = f;
+                if (by_pos) fetch_pos(k0 + kStep);
                 const int buf = cnt & 1;
                 const uint32_t sa = tm + lane_off + TM_S + x * 128 + buf * kSub;
                 wait(B_SFULL + 2 * x + buf, (cnt >> 1) & 1, 89);
@@ -576,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (work) {
                     float v[64];
                     tmem_ld64(sa, v);
-                    if (!__all_sync(kAll, vis == ~0ull)) {
+                    if (masked) {
                         const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
@@ -586,7 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+                    for (int i = 4; i < 60; i += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], v[i + e]), v[i + 4 + e]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], v[60 + e]);
                     const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                     float alpha = 1.f;
                     bool rescale = false;
@@ -598,16 +627,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = mb;
                     }
                     const float msub = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t cc = pack_f32x2(c, c), mm = pack_f32x2(-msub, -msub);
+                    uint64_t sum[4] = {0, 0, 0, 0};
                     uint32_t pk[32];
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
-                        const float e0 = ex2_approx(fmaf(v[i], c, -msub)), e1 = ex2_approx(fmaf(v[i + 1], c, -msub));
-                        sum[(i >> 1) & 3] += e0 + e1;
+                        float e0, e1;
+                        unpack_f32x2(fma_f32x2(pack_f32x2(v[i], v[i + 1]), cc, mm), e0, e1);
+                        e0 = ex2_approx(e0);
+                        e1 = ex2_approx(e1);
+                        sum[(i >> 1) & 3] = add_f32x2(sum[(i >> 1) & 3], pack_f32x2(e0, e1));
                         pk[i >> 1] = pack_bf16(e0, e1);
                     }
                     tmem_st32u(sa, pk);
-                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    float s0, s1;
+                    unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), s0, s1);
+                    l = fmaf(l, alpha, s0 + s1);
                     if (__any_sync(kAll, rescale)) {    // once P V of the half block before has completed
                         if (cnt > cnt0) wait_pv(cnt - 1, 90);
                         tc_fence_after();
@@ -621,18 +656,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                // V rows behind the last key, up to the 16 of a product step, may hold
-                // anything; P is zero there and the rows are cleared (by rows both
-                // streams write the same zeros, each before its own product)
-                const int behind = valid < kSub ? (16 - valid % 16) % 16 : 0;
-                if (behind) {
-                    const int s = at % NST;
-                    wait(B_VFULL + s, (at / NST) & 1, 91);
-                    for (int e = gtid; e < behind * 16; e += 128) {
-                        const int row = kSub * h + valid + e / 16, ch = e % 16;
-                        st_shared_v4(smem_u32(sm + C::kV + s * kBlk + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16), 0, 0, 0, 0);
+                if (special) {
+                    // V rows behind the last key, up to the 16 of a product step, may hold
+                    // anything; P is zero there and the rows are cleared (by rows both
+                    // streams write the same zeros, each before its own product)
+                    const int behind = (16 - valid % 16) % 16, at = used + j - seg.blk0;
+                    if (behind) {
+                        const int s = at % NST;
+                        wait(B_VFULL + s, (at / NST) & 1, 91);
+                        for (int e = gtid; e < behind * 16; e += 128) {
+                            const int row = kSub * h + valid + e / 16, ch = e % 16;
+                            st_shared_v4(smem_u32(sm + C::kV + s * kBlk + (ch >> 3) * kHalf + row * 128 + (ch & 7) * 16), 0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
+                    a.step(seg);
                 }
                 ++cnt;
                 tc_fence_before();
