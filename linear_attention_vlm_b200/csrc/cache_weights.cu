@@ -144,10 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctl + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(ctl + kOffAbort);
     int *err_sh = reinterpret_cast<int *>(ctl + kOffErr);
-    auto fail = [&](int code) {
-        *abort_flag = 1;
-        atomicCAS(err_sh, 0, code);
-    };
+    auto fail = [&](int code) { record_failure(abort_flag, err_sh, code); };
 
     // ---------------------------------------------------------------- plan (as in tree_attention.cu)
     int64_t *plan = reinterpret_cast<int64_t *>(ctl + kOffPlan);
