@@ -34,13 +34,13 @@ namespace gdn {
 namespace {
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -49,6 +49,11 @@ __device__ __forceinline__ float4 load_stream(const float *p) {   // read once: 
     float4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
     return v;
+}
+
+// 16 bytes to shared memory without passing a register; zeros where `there` is false.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -212,15 +217,22 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, NP <= 16 ? 2 : 1)
             s1[s] = L.state ? load_stream(row + 8 * D + 16 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
-    // keys, queries and values; rows behind the last node are zero
+    // keys, queries and values, all copies in flight at once; rows behind the last node are zero
     {
         constexpr int V = 16 / sizeof(T), per = D / V;
-        for (int e = tid; e < 3 * NP * per; e += S::kThreads) {
-            const int m = e / (NP * per), i = e / per % NP, c = e % per * V;
-            const T *src = static_cast<const T *>(m == 0 ? L.k : m == 1 ? L.q : L.v) + ((bos + i) * L.H + h) * D + c;
-            const uint4 x = i < n ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(m < 2 ? kq + (m * NP + i) * S::kRow + c : vo + i * S::kVRow + c) = x;
+        const int64_t step = (int64_t)L.H * D;
+        const int64_t first = bos * step + (int64_t)h * D;
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+            const T *src = static_cast<const T *>(m == 0 ? L.k : m == 1 ? L.q : L.v) + first;
+            T *dst = m == 0 ? kq : m == 1 ? kq + NP * S::kRow : vo;
+            const int row = m < 2 ? S::kRow : S::kVRow;
+            for (int e = tid; e < NP * per; e += S::kThreads) {
+                const int i = e / per, c = e % per * V;
+                copy16(dst + i * row + c, src + min(i, n - 1) * step + c, i < n);
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
     if (!main_warp) {
         // ancestors and path sums by doubling: every round a node takes over
@@ -259,40 +271,44 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, NP <= 16 ? 2 : 1)
             anc[i] = a;
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 
     // A and P: products of keys and queries with keys, decayed, 0 where j is no ancestor
     const int tiles = (n + 7) / 8;   // 8 nodes each
-    if (main_warp) {
+    {
+        // tiles of 16 rows (keys, then queries) by 8 keys, dealt to all warps
+        constexpr int MT = NP / 16, JT = NP / 8;
 #pragma unroll 1
-        for (int mt = warp; mt < 2 * NP / 16; mt += S::kMain) {
-            const bool reads = mt >= NP / 16;                       // a tile of queries
-            const int i0 = (mt % (NP / 16)) * 16;
+        for (int w = warp; w < 2 * MT * JT; w += S::kThreads / 32) {
+            const int mt = w / JT, j0 = w % JT * 8, i0 = mt % MT * 16;
+            const bool reads = mt >= MT;                            // a tile of queries
             if (i0 >= n) continue;
-            const T *r0 = kq + (mt * 16 + g) * S::kRow + 4 * t, *r1 = r0 + 8 * S::kRow;
-            const int i[2] = {i0 + g, i0 + g + 8};
-            const unsigned long long an[2] = {anc[i[0]], anc[i[1]]};
-            const float G[2] = {Gs[i[0]], Gs[i[1]]}, be[2] = {bs[i[0]], bs[i[1]]};
-#pragma unroll 1
-            for (int j0 = 0; j0 < NP; j0 += 8) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                if (j0 < i0 + 16) {                                // ancestors come before
-                    const T *rb = kq + (j0 + g) * S::kRow + 4 * t;
+            float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            if (j0 < i0 + 16) {                                    // ancestors come before
+                const T *r0 = kq + (mt * 16 + g) * S::kRow + 4 * t, *r1 = r0 + 8 * S::kRow;
+                const T *rb = kq + (j0 + g) * S::kRow + 4 * t;
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) {
-                        typename F::B fb;
-                        F::load_b(rb + 16 * s, fb);
-                        F::mma_rows(c, r0 + 16 * s, r1 + 16 * s, fb);
-                    }
+                for (int s = 0; s < KS; ++s) {
+                    typename F::B fb;
+                    F::load_b(rb + 16 * s, fb);
+                    F::mma_rows(c[s & 1], r0 + 16 * s, r1 + 16 * s, fb);
                 }
+            }
+            const float2 Gj = *reinterpret_cast<const float2 *>(Gs + j0 + 2 * t);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = j0 + 2 * t + (e & 1), r = e >> 1;
-                    const bool see = (an[r] >> j & 1) && (reads || j != i[r]);
-                    const float v = see ? c[e] * F::exp(G[r] - Gs[j]) : 0.f;
-                    if (reads) ps[i[r] * S::kP + j] = v;
-                    else as[i[r] * S::kA + j] = v * be[r];
+            for (int r = 0; r < 2; ++r) {
+                const int i = i0 + g + 8 * r, j = j0 + 2 * t;
+                const unsigned two = (unsigned)(anc[i] >> j) & 3u;
+                const float G = Gs[i];
+                float x = two & 1 ? (c[0][2 * r] + c[1][2 * r]) * F::exp(G - Gj.x) : 0.f;
+                float y = two & 2 ? (c[0][2 * r + 1] + c[1][2 * r + 1]) * F::exp(G - Gj.y) : 0.f;
+                if (!reads) {
+                    const float be = bs[i];
+                    x = j == i ? 0.f : x * be;
+                    y = j + 1 == i ? 0.f : y * be;
                 }
+                *reinterpret_cast<float2 *>(reads ? ps + i * S::kP + j : as + i * S::kA + j) = make_float2(x, y);
             }
         }
     }

@@ -517,15 +517,19 @@ def gdn_swa_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
 MAX_TREE_NODES = 64
 
 
-def _arg(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev) -> Optional[int]:
-    """The address of a contiguous tensor of this shape and type on ``dev``."""
+def _refuse(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev) -> None:
     if t is None:
         raise ValueError("%s is missing" % what)
     if t.shape != shape or t.dtype is not dtype or t.device != dev:
         raise ValueError("%s must be %s %s on %s" % (what, dtype, list(shape), dev))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
-    return t.data_ptr() or None
+    raise ValueError("%s must be contiguous" % what)
+
+
+def _arg(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev) -> int:
+    """The address of a contiguous tensor of this shape and type on ``dev``."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _refuse(what, t, shape, dtype, dev)
+    return t.data_ptr()
 
 
 def _opt(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev) -> Optional[int]:
@@ -540,12 +544,9 @@ def _scratch(workspace: Optional[torch.Tensor], need: int, dev) -> Tuple[torch.T
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _on_device(dev, fn, *args) -> int:
-    """fn(*args, current stream of dev), with dev current."""
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, _stream(dev))
-    with torch.cuda.device(dev):
-        return fn(*args, _stream(dev))
+def _current(dev):
+    """A guard under which ``dev`` is current, or None where it is already."""
+    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _tree_nodes(max_nodes: Optional[int], cu: Optional[torch.Tensor], T: int, B: int) -> int:
@@ -602,14 +603,21 @@ def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent
     code = _dtype_code(dt)
     ws, ws_bytes = _scratch(workspace, _tree_attention_ws(B, T, n, cap, Hq, Hkv, d, code), dev)
     i32, new, old = torch.int32, (T, Hkv, d), (B, cap, Hkv, d)
-    st = _on_device(
-        dev, _load().gdn_tree_attention, _arg("q", q, q.shape, dt, dev), _arg("k", k, new, dt, dev),
+    args = (
+        _arg("q", q, q.shape, dt, dev), _arg("k", k, new, dt, dev),
         _arg("v", v, new, dt, dev), _opt("parents", parents, (T,), i32, dev),
         _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), _arg("k_cache", k_cache, old, dt, dev),
         _arg("v_cache", v_cache, old, dt, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
         _opt("cache_pos", cache_pos, (B, Hkv, cap), i32, dev), _opt("seen", seen, (B,), i32, dev),
         _arg("out", out, q.shape, dt, dev), _arg("lse", lse, (T, Hq), torch.float32, dev), B, T, n, cap, Hq, Hkv, d,
-        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes)
+        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
+        _stream(dev))
+    guard = _current(dev)
+    if guard is None:
+        st = _load().gdn_tree_attention(*args)
+    else:
+        with guard:
+            st = _load().gdn_tree_attention(*args)
     if st != GDN_OK:
         raise GdnError(st, "gdn_tree_attention")
     return out, lse
@@ -632,12 +640,19 @@ def gdn_tree_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     if out is None:
         out = torch.empty_like(v)
     i32, f32, rows = torch.int32, torch.float32, (T, H, d)
-    st = _on_device(
-        dev, _load().gdn_tree_step, _arg("q", q, rows, dt, dev), _arg("k", k, rows, dt, dev),
+    args = (
+        _arg("q", q, rows, dt, dev), _arg("k", k, rows, dt, dev),
         _arg("v", v, rows, dt, dev), _arg("g", g, (T, H), f32, dev), _arg("beta", beta, (T, H), f32, dev),
         _opt("parents", parents, (T,), i32, dev), _arg("state", state, (B, H, d, d), f32, dev),
         _arg("out", out, rows, dt, dev), _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, n, H, d, d,
-        _dtype_code(dt))
+        _dtype_code(dt),
+        _stream(dev))
+    guard = _current(dev)
+    if guard is None:
+        st = _load().gdn_tree_step(*args)
+    else:
+        with guard:
+            st = _load().gdn_tree_step(*args)
     if st != GDN_OK:
         raise GdnError(st, "gdn_tree_step")
     return out
@@ -673,14 +688,21 @@ def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cac
     code = _dtype_code(dt)
     ws, ws_bytes = _scratch(workspace, _cache_weights_ws(B, Tq, T, cap, Hq, Hkv, d, code), dev)
     i32, f32, cells = torch.int32, torch.float32, (B, Hkv, cap)
-    st = _on_device(
-        dev, _load().gdn_cache_weights, _arg("q", q, q.shape, dt, dev), _arg("lse", lse, (Tq, Hq), f32, dev),
+    args = (
+        _arg("q", q, q.shape, dt, dev), _arg("lse", lse, (Tq, Hq), f32, dev),
         _arg("k", k, (T, Hkv, d), dt, dev), _arg("k_cache", k_cache, (B, cap, Hkv, d), dt, dev),
         _arg("weights", weights, cells, f32, dev), _arg("weights_out", weights_out, cells, f32, dev),
         _arg("new_weights", new_weights, (T, Hkv), f32, dev), _opt("cu_queries", cu_queries, (B + 1,), i32, dev),
         _opt("cu_tokens", cu_tokens, (B + 1,), i32, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
         _opt("cache_pos", cache_pos, cells, i32, dev), _opt("seen", seen, (B,), i32, dev), B, Tq, T, cap, Hq, Hkv, d,
-        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes)
+        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
+        _stream(dev))
+    guard = _current(dev)
+    if guard is None:
+        st = _load().gdn_cache_weights(*args)
+    else:
+        with guard:
+            st = _load().gdn_cache_weights(*args)
     if st != GDN_OK:
         raise GdnError(st, "gdn_cache_weights")
     return weights_out, new_weights
@@ -711,8 +733,8 @@ def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
     i32, f32, rows, cells = torch.int32, torch.float32, (T, Hkv, d), (B, Hkv, cap)
     w, p = _arg("weights", weights, cells, f32, dev), _arg("cache_pos", cache_pos, cells, i32, dev)
     ln, sn = _arg("cache_lens", cache_lens, (B,), i32, dev), _arg("seen", seen, (B,), i32, dev)
-    st = _on_device(
-        dev, _load().gdn_cache_insert, _arg("k", k, rows, dt, dev), _arg("v", v, rows, dt, dev),
+    args = (
+        _arg("k", k, rows, dt, dev), _arg("v", v, rows, dt, dev),
         _arg("k_cache", k_cache, (B, cap, Hkv, d), dt, dev), _arg("v_cache", v_cache, (B, cap, Hkv, d), dt, dev),
         w, w if weights_out is None else _arg("weights_out", weights_out, cells, f32, dev),
         p, p if pos_out is None else _arg("pos_out", pos_out, cells, i32, dev),
@@ -720,7 +742,14 @@ def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
         sn, sn if seen_out is None else _arg("seen_out", seen_out, (B,), i32, dev),
         _opt("new_weights", new_weights, (T, Hkv), f32, dev), _arg("slots", slots, (T, Hkv), i32, dev),
         _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, cap, Hkv, d, int(recent), code, ws.data_ptr(),
-        ws_bytes)
+        ws_bytes,
+        _stream(dev))
+    guard = _current(dev)
+    if guard is None:
+        st = _load().gdn_cache_insert(*args)
+    else:
+        with guard:
+            st = _load().gdn_cache_insert(*args)
     if st != GDN_OK:
         raise GdnError(st, "gdn_cache_insert")
     return (weights if weights_out is None else weights_out, cache_pos if pos_out is None else pos_out,
