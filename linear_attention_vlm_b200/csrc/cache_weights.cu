@@ -47,7 +47,7 @@ constexpr int kSumWarps = 16, kProducerWarp = 16, kMmaWarp = 17, kThreads = 32 *
 constexpr uint32_t SM_K = 0, SM_Q = kKStages * kBlk, SM_CTL = SM_Q + kQSlots * kBlk;
 enum : int { B_KFULL = 0, B_KEMPTY = B_KFULL + kKStages, B_QFULL = B_KEMPTY + kKStages, B_QEMPTY = B_QFULL + kQSlots,
              B_SFULL = B_QEMPTY + kQSlots, B_SEMPTY = B_SFULL + 4, B_FIN = B_SEMPTY + 4, B_NUM };
-constexpr uint32_t kOffTmem = 8 * B_NUM, kOffAbort = kOffTmem + 4, kOffErr = kOffTmem + 8, kOffPlan = 192;
+constexpr uint32_t kOffTmem = 8 * B_NUM, kOffAbort = kOffTmem + 4, kOffErr = kOffTmem + 8, kOffPlan = 192;   // units, index, Seq
 constexpr uint32_t kOffLse = 256;                              // [2 streams][slots][128] fp32: lse log2(e)
 constexpr uint32_t kOffPos = kOffLse + 2 * kQSlots * 512;      // [2][slots][128] int32: positions of the rows' queries
 constexpr uint32_t kOffXch = kOffPos + 2 * kQSlots * 512;      // [2][128] fp32
@@ -98,9 +98,8 @@ struct Walk {
     int b;
     Seq s;
     int h, blk0, blk1;
-    __device__ Walk(const Params &p_, int64_t w_, int64_t end_, int b_, int64_t base_) : p(p_), w(w_), end(end_), base(base_), b(b_) {
-        if (w < end) s = load_seq(p, b);
-    }
+    __device__ Walk(const Params &p_, int64_t w_, int64_t end_, int b_, int64_t base_, const Seq &s_)
+        : p(p_), w(w_), end(end_), base(base_), b(b_), s(s_) {}
     __device__ __forceinline__ bool next() {
         while (w < end) {
             int64_t share;
@@ -146,47 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *err_sh = reinterpret_cast<int *>(ctl + kOffErr);
     auto fail = [&](int code) { record_failure(abort_flag, err_sh, code); };
 
-    // ---------------------------------------------------------------- plan (as in tree_attention.cu)
-    int64_t *plan = reinterpret_cast<int64_t *>(ctl + kOffPlan);
-    int64_t *wsum = reinterpret_cast<int64_t *>(sm);
-    int64_t W = 0;
-    for (int b = tid; b < p.num_seqs; b += kThreads) W += load_seq(p, b).work(p.Hkv);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(kAll, W, o);
-    if (lane == 0) wsum[warp] = W;
-    __syncthreads();
-    W = 0;
-    for (int i = 0; i < kThreads / 32; ++i) W += wsum[i];
-    const int64_t w0 = W * cta / gridDim.x, w1 = W * (cta + 1) / gridDim.x;
-    int64_t carry = 0;
-    for (int b0 = 0; b0 < p.num_seqs && carry <= w0; b0 += kThreads) {
-        const int b = b0 + tid;
-        const int64_t mine = b < p.num_seqs ? load_seq(p, b).work(p.Hkv) : 0;
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t t = __shfl_up_sync(kAll, incl, o);
-            if (lane >= o) incl += t;
-        }
-        __syncthreads();
-        if (lane == 31) wsum[warp] = incl;
-        __syncthreads();
-        int64_t before = carry;
-        for (int i = 0; i < warp; ++i) before += wsum[i];
-        for (int i = 0; i < kThreads / 32; ++i) carry += wsum[i];
-        const int64_t start = before + incl - mine;
-        if (mine > 0 && start <= w0 && w0 < start + mine) {
-            plan[0] = start;
-            plan[1] = b;
-        }
-    }
-    if (w0 == w1) return;
-
     if (warp == 0) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
     if (tid == 32 * kProducerWarp) {
+        tma_prefetch_desc(&mQ);
+        tma_prefetch_desc(&mKc);
+        tma_prefetch_desc(&mKn);
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(bar(B_KFULL + s), 1);
             mbar_init(bar(B_KEMPTY + s), 1);
@@ -204,12 +170,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         *err_sh = 0;
         fence_mbar_init();
     }
+
+    // ---------------------------------------------------------------- plan (as in tree_attention.cu)
+    int64_t *plan = reinterpret_cast<int64_t *>(ctl + kOffPlan);                // units before the first sequence, its index
+    Seq *plan_seq = reinterpret_cast<Seq *>(plan + 2);
+    static_assert(16 + sizeof(Seq) <= kOffLse - kOffPlan, "plan area");
+    int64_t *wsum = reinterpret_cast<int64_t *>(sm);                            // [18] scratch before any copy lands
+    int64_t W = 0, w0 = 0, w1 = 0;
+    const bool one_pass = p.num_seqs <= kThreads;
+    if (!one_pass) {   // the total first
+        for (int b = tid; b < p.num_seqs; b += kThreads) W += load_seq(p, b).work(p.Hkv);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(kAll, W, o);
+        if (lane == 0) wsum[warp] = W;
+        __syncthreads();
+        W = 0;
+        for (int i = 0; i < kThreads / 32; ++i) W += wsum[i];
+    }
+    auto my_run = [&] {
+        w0 = W * cta / gridDim.x;
+        w1 = W * (cta + 1) / gridDim.x;
+    };
+    my_run();
+    int64_t carry = 0;
+    for (int b0 = 0; b0 < p.num_seqs && carry <= w0; b0 += kThreads) {
+        const int b = b0 + tid;
+        Seq s;
+        int64_t mine = 0;
+        if (b < p.num_seqs) {
+            s = load_seq(p, b);
+            mine = s.work(p.Hkv);
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t t = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += t;
+        }
+        __syncthreads();
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        int64_t before = carry;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += wsum[i];
+            carry += wsum[i];
+        }
+        if (one_pass) {
+            W = carry;
+            my_run();
+        }
+        const int64_t start = before + incl - mine;
+        if (mine > 0 && start <= w0 && w0 < start + mine) {
+            plan[0] = start;
+            plan[1] = b;
+            *plan_seq = s;
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = *tmem_slot;
     const uint64_t lim = p.timeout_ns, drain = p.drain_ns;
-    Walk seg(p, w0, w1, (int)plan[1], plan[0]);
+    if (w0 < w1) {
+    Walk seg(p, w0, w1, (int)plan[1], plan[0], *plan_seq);
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------------ TMA producer
@@ -237,6 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (chunks == 0) continue;
                 const bool resident = chunks <= kQSlots;
                 for (int j = seg.blk0; ok && j < seg.blk1; j += 2) {
+                    if (resident && j == seg.blk0)
+                        for (int c = 0; ok && c < chunks; ++c) ok = load_q(c);
                     for (int x = 0; x < 2 && j + x < seg.blk1; ++x, ++keys) {
                         const int s = keys % kKStages;
                         if (keys >= kKStages && !wait_phase(bar(B_KEMPTY + s), ((keys - kKStages) / kKStages) & 1, lim, abort_flag)) {
@@ -252,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(smem_u32(sm + SM_K + s * kBlk + kHalf), m, 64, seg.h, row, bar(B_KFULL + s));
                         ++issued_k[s];
                     }
-                    if (!resident || j == seg.blk0)
+                    if (!resident)
                         for (int c = 0; ok && c < chunks; ++c) ok = load_q(c);
                 }
             }
@@ -424,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 named_bar_sync(bar_pair, 64);
             }
         }
+    }
     }
     tc_fence_before();
     __syncthreads();
