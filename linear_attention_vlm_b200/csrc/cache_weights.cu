@@ -16,14 +16,14 @@
 //
 // All (sequence, key/value head, key block) units are laid end to end, each
 // weighted by its row chunks, and cut evenly over one persistent CTA per SM.
-// A CTA works on two key blocks at a time, one per stream of 8 warps, so a chunk of
-// 128 query rows serves both.  Up to two chunks stay in shared memory for a
-// whole item; longer query lists stream through the same slots.
-//   warps 0-7 / 8-15  sums of stream 0 / 1 (warps w and w + 4 share the keys of
-//                     TMEM lane quarter w % 4, each takes every other 32 columns)
-//   warp 16           TMA producer
-//   warp 17           MMA issuer (one lane)
-// Tensor memory: 2 streams x 2 buffers x 128 columns.
+// Four groups of 4 warps take the key blocks in turn, each with its own 128
+// columns of tensor memory, so that a block's sums need no exchange and the groups'
+// special-function work fills the gaps of one another.  Up to two chunks of 128 query
+// rows stay in shared memory for a whole item; longer query lists stream through
+// the same slots, once for four blocks.
+//   warps 0-15  sums: group w / 4, the keys of TMEM lane quarter w % 4
+//   warp 16     TMA producer
+//   warp 17     MMA issuer
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,16 +42,16 @@ constexpr int kD = 128, kKeys = 128, kRows = 128;
 constexpr uint32_t kHalf = 16384, kBlk = 2 * kHalf;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKStages = 4, kQSlots = 2;
+constexpr int kGroups = 4;
 constexpr int kSumWarps = 16, kProducerWarp = 16, kMmaWarp = 17, kThreads = 32 * 18;
 
 constexpr uint32_t SM_K = 0, SM_Q = kKStages * kBlk, SM_CTL = SM_Q + kQSlots * kBlk;
 enum : int { B_KFULL = 0, B_KEMPTY = B_KFULL + kKStages, B_QFULL = B_KEMPTY + kKStages, B_QEMPTY = B_QFULL + kQSlots,
              B_SFULL = B_QEMPTY + kQSlots, B_SEMPTY = B_SFULL + 4, B_FIN = B_SEMPTY + 4, B_NUM };
 constexpr uint32_t kOffTmem = 8 * B_NUM, kOffAbort = kOffTmem + 4, kOffErr = kOffTmem + 8, kOffPlan = 192;   // units, index, Seq
-constexpr uint32_t kOffLse = 256;                              // [2 streams][slots][128] fp32: lse log2(e)
-constexpr uint32_t kOffPos = kOffLse + 2 * kQSlots * 512;      // [2][slots][128] int32: positions of the rows' queries
-constexpr uint32_t kOffXch = kOffPos + 2 * kQSlots * 512;      // [2][128] fp32
-constexpr size_t kSmem = SM_CTL + kOffXch + 1024 + 1024;
+constexpr uint32_t kOffLse = 256;                              // [groups][slots][128] fp32: lse log2(e)
+constexpr uint32_t kOffPos = kOffLse + kGroups * kQSlots * 512;   // the same, int32: positions of the rows' queries
+constexpr size_t kSmem = SM_CTL + kOffPos + kGroups * kQSlots * 512 + 1024;
 static_assert(kOffErr + 4 <= kOffPlan, "barrier area");
 static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t kTmemCols = 512;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 4; ++s) {
             mbar_init(bar(B_SFULL + s), 1);
-            mbar_init(bar(B_SEMPTY + s), 32 * kSumWarps / 2);
+            mbar_init(bar(B_SEMPTY + s), 32 * kSumWarps / kGroups);
         }
         mbar_init(bar(B_FIN), 1);
         *abort_flag = 0;
@@ -259,10 +259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int chunks = seg.s.chunks;
                 if (chunks == 0) continue;
                 const bool resident = chunks <= kQSlots;
-                for (int j = seg.blk0; ok && j < seg.blk1; j += 2) {
+                for (int j = seg.blk0; ok && j < seg.blk1; j += kGroups) {
                     if (resident && j == seg.blk0)
                         for (int c = 0; ok && c < chunks; ++c) ok = load_q(c);
-                    for (int x = 0; x < 2 && j + x < seg.blk1; ++x, ++keys) {
+                    for (int x = 0; x < kGroups && j + x < seg.blk1; ++x, ++keys) {
                         const int s = keys % kKStages;
                         if (keys >= kKStages && !wait_phase(bar(B_KEMPTY + s), ((keys - kKStages) / kKStages) & 1, lim, abort_flag)) {
                             fail(102);
@@ -289,72 +289,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint64_t dKm = desc_sw128(smem_u32(sm), 16, 1024);
-            int keys = 0, loads = 0, cnt[2] = {0, 0};   // cnt: products per stream
-            bool ok = true;
-            auto wait = [&](int b, uint32_t parity, int code) {
-                if (!wait_phase(bar(b), parity, lim, abort_flag)) {
-                    fail(code);
-                    ok = false;
-                }
-                return ok;
-            };
-            while (ok && seg.next()) {
-                const int chunks = seg.s.chunks;
-                if (chunks == 0) continue;
-                const bool resident = chunks <= kQSlots;
-                for (int j = seg.blk0; ok && j < seg.blk1; j += 2) {
-                    const int two = min(2, seg.blk1 - j);
-                    for (int x = 0; x < two; ++x)
-                        if (!wait(B_KFULL + (keys + x) % kKStages, ((keys + x) / kKStages) & 1, 103)) break;
-                    for (int c = 0; ok && c < chunks; ++c) {
-                        const int load = loads + c, s = load % kQSlots;
-                        if (!wait(B_QFULL + s, (load / kQSlots) & 1, 104)) break;
-                        const int n = min(kRows, (seg.rows(c) + 15) & ~15);
-                        const uint32_t id = idesc_bf16(kKeys, n, false, false);
-                        for (int x = 0; x < two; ++x) {
-                            if (seg.skip(j + x, c)) continue;
-                            const int buf = 2 * x + (cnt[x] & 1);
-                            if (cnt[x] >= 2 && !wait(B_SEMPTY + buf, ((cnt[x] - 2) >> 1) & 1, 105)) break;
-                            tc_fence_after();
-                            const uint32_t kofs = SM_K + ((keys + x) % kKStages) * kBlk, qofs = SM_Q + s * kBlk;
+        const uint64_t dKm = desc_sw128(smem_u32(sm), 16, 1024);
+        int keys = 0, loads = 0, blocks = 0, cnt[kGroups] = {0, 0, 0, 0};   // cnt: products per group
+        bool ok = true;
+        auto wait = [&](int b, uint32_t parity, int code) {
+            if (!__all_sync(kAll, wait_phase(bar(b), parity, lim, abort_flag))) {
+                fail(code);
+                ok = false;
+            }
+            return ok;
+        };
+        // S^T = K Q^T of the block in K stage `key` and the chunk in slot `slot`, for group g
+        auto product = [&](int g, int key, int slot, int rows) {
+            int n = 0;   // products of this group so far (no dynamic indexing of registers)
 #pragma unroll
-                            for (int ks = 0; ks < kD / 16; ++ks) {
-                                const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-                                mma_bf16_ss(tm + buf * kRows, dKm + ((kofs + off) >> 4), dKm + ((qofs + off) >> 4), id, ks > 0);
-                            }
-                            mma_commit(bar(B_SFULL + buf));
-                            ++cnt[x];
-                        }
-                        if (!resident) mma_commit(bar(B_QEMPTY + s));
-                    }
-                    for (int x = 0; x < two; ++x) mma_commit(bar(B_KEMPTY + (keys + x) % kKStages));
-                    keys += two;
-                    if (!resident) loads += chunks;
+            for (int i = 0; i < kGroups; ++i)
+                if (i == g) n = cnt[i]++;
+            if (n && !wait(B_SEMPTY + g, (n - 1) & 1, 105)) return;
+            tc_fence_after();
+            const uint32_t id = idesc_bf16(kKeys, min(kRows, (rows + 15) & ~15), false, false);
+            const uint64_t kd = dKm + ((SM_K + key * kBlk) >> 4), qd = dKm + ((SM_Q + slot * kBlk) >> 4);
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < kD / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                    mma_bf16_ss(tm + g * kRows, kd + off, qd + off, id, ks > 0);
                 }
-                if (resident) {
-                    for (int c = 0; c < chunks; ++c) mma_commit(bar(B_QEMPTY + (loads + c) % kQSlots));
-                    loads += chunks;
+                mma_commit(bar(B_SFULL + g));
+            }
+            __syncwarp();
+        };
+        auto free_stage = [&](int b) {
+            if (elect_one()) mma_commit(bar(b));
+            __syncwarp();
+        };
+        while (ok && seg.next()) {
+            const int chunks = seg.s.chunks, nblk = seg.blk1 - seg.blk0;
+            if (chunks == 0) {
+                blocks += nblk;
+                continue;
+            }
+            if (chunks <= kQSlots) {   // all chunks stay
+                for (int c = 0; ok && c < chunks; ++c) wait(B_QFULL + (loads + c) % kQSlots, ((loads + c) / kQSlots) & 1, 104);
+                for (int j = seg.blk0; ok && j < seg.blk1; ++j, ++keys, ++blocks) {
+                    if (!wait(B_KFULL + keys % kKStages, (keys / kKStages) & 1, 103)) break;
+                    for (int c = 0; ok && c < chunks; ++c)
+                        if (!seg.skip(j, c)) product(blocks % kGroups, keys % kKStages, (loads + c) % kQSlots, seg.rows(c));
+                    free_stage(B_KEMPTY + keys % kKStages);
+                }
+                for (int c = 0; c < chunks; ++c) free_stage(B_QEMPTY + (loads + c) % kQSlots);
+                loads += chunks;
+            } else {
+                for (int j = seg.blk0; ok && j < seg.blk1; j += kGroups) {
+                    const int many = min(kGroups, seg.blk1 - j);
+                    for (int x = 0; ok && x < many; ++x) wait(B_KFULL + (keys + x) % kKStages, ((keys + x) / kKStages) & 1, 103);
+                    for (int c = 0; ok && c < chunks; ++c, ++loads) {
+                        if (!wait(B_QFULL + loads % kQSlots, (loads / kQSlots) & 1, 104)) break;
+                        for (int x = 0; ok && x < many; ++x)
+                            if (!seg.skip(j + x, c)) product((blocks + x) % kGroups, (keys + x) % kKStages, loads % kQSlots, seg.rows(c));
+                        free_stage(B_QEMPTY + loads % kQSlots);
+                    }
+                    for (int x = 0; x < many; ++x) free_stage(B_KEMPTY + (keys + x) % kKStages);
+                    keys += many;
+                    blocks += many;
                 }
             }
-            mma_commit(bar(B_FIN));   // every issued MMA completes before TMEM is released
-            const int zero = 0;
-            wait_phase(bar(B_FIN), 0, drain, &zero);
         }
+        free_stage(B_FIN);   // every issued MMA completes before TMEM is released
+        const int zero = 0;
+        wait_phase(bar(B_FIN), 0, drain, &zero);
     } else {
         // ------------------------------------------------------------ sums (warps 0-15)
         // As in tree_attention.cu, a wait that gives up does not leave the loops.
-        const int x = warp >> 3, quarter = warp & 3, half = (warp >> 2) & 1, gtid = tid & 255;
-        const int r = 32 * quarter + lane;   // the key of this thread
-        const uint32_t sa = tm + (static_cast<uint32_t>(32 * quarter) << 16) + x * 2 * kRows;
-        float *lse_sh = reinterpret_cast<float *>(ctl + kOffLse) + x * kQSlots * kRows;
-        int *pos_sh = reinterpret_cast<int *>(ctl + kOffPos) + x * kQSlots * kRows;
-        float *xch = reinterpret_cast<float *>(ctl + kOffXch) + x * kRows;
-        const int bar_pair = 1 + 4 * x + quarter, bar_group = 9 + x;
+        const int grp = warp >> 2, gtid = tid & 127;
+        const int r = gtid;   // the key of this thread = TMEM lane
+        const uint32_t sa = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + grp * kRows;
+        float *lse_sh = reinterpret_cast<float *>(ctl + kOffLse) + grp * kQSlots * kRows;
+        int *pos_sh = reinterpret_cast<int *>(ctl + kOffPos) + grp * kQSlots * kRows;
+        const int bar_group = 1 + grp;
         const float c2 = p.c;
         bool ok = true;
-        int cnt = 0;
+        int cnt = 0, blocks = 0;
         while (seg.next()) {
             const Seq &s = seg.s;
             const int chunks = s.chunks;
@@ -362,62 +377,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             // positions count from the first new token
             const int64_t seen = p.pos ? p.seen[seg.b] : s.len;
             auto fetch = [&](int c) {   // lse and position of row gtid of chunk c, into its slot
-                if (gtid < kRows) {
-                    float l = INFINITY;
-                    if (gtid < seg.rows(c)) {
-                        const int64_t row = (s.q0 + c * p.chunk_q + gtid / p.group) * p.Hq + (int64_t)seg.h * p.group + gtid % p.group;
-                        l = p.lse[row];
-                        l = l == -INFINITY ? INFINITY : l * kLog2e;
-                    }
-                    lse_sh[(c % kQSlots) * kRows + gtid] = l;
-                    pos_sh[(c % kQSlots) * kRows + gtid] = s.m - s.nq + c * p.chunk_q + gtid / p.group;
+                float l = INFINITY;
+                if (gtid < seg.rows(c)) {
+                    const int64_t row = (s.q0 + c * p.chunk_q + gtid / p.group) * p.Hq + (int64_t)seg.h * p.group + gtid % p.group;
+                    l = p.lse[row];
+                    l = l == -INFINITY ? INFINITY : l * kLog2e;
                 }
+                lse_sh[(c % kQSlots) * kRows + gtid] = l;
+                pos_sh[(c % kQSlots) * kRows + gtid] = s.m - s.nq + c * p.chunk_q + gtid / p.group;
             };
             if (resident) {
-                named_bar_sync(bar_group, 256);
+                named_bar_sync(bar_group, 128);
                 for (int c = 0; c < chunks; ++c) fetch(c);
-                named_bar_sync(bar_group, 256);
+                named_bar_sync(bar_group, 128);
             }
-            for (int j = seg.blk0 + x; j < seg.blk1; j += 2) {
+            for (int j = seg.blk0 + (grp - blocks % kGroups + kGroups) % kGroups; j < seg.blk1; j += kGroups) {
                 const bool old = seg.old(j), mine = r < seg.valid(j);
                 const int key = seg.key0(j) + r;
                 const int64_t slot = ((int64_t)seg.b * p.Hkv + seg.h) * p.capacity + key;
                 float before = 0.f;
-                if (half == 0 && old && mine) before = p.w_in[slot];
+                if (old && mine) before = p.w_in[slot];
                 // a slot's position, seen from the first new token; never behind the first query
                 int kp = 0;
-                if (mine) {
-                    if (!old) kp = key;
-                    else if (p.window != INT32_MAX)
-                        kp = (int)max((int64_t)INT32_MIN / 2, min((int64_t)(s.m - s.nq), (p.pos ? (int64_t)p.pos[slot] : key) - seen));
+                bool all = true;   // whether every row sees every key of the warp
+                if (!old || p.window != INT32_MAX) {
+                    if (mine) {
+                        if (!old) kp = key;
+                        else
+                            kp = (int)max((int64_t)INT32_MIN / 2, min((int64_t)(s.m - s.nq), (p.pos ? (int64_t)p.pos[slot] : key) - seen));
+                    }
+                    all = false;
                 }
-                const int kmin = __reduce_min_sync(kAll, mine ? kp : INT32_MAX), kmax = __reduce_max_sync(kAll, mine ? kp : INT32_MIN);
+                const int kmin = all ? 0 : __reduce_min_sync(kAll, mine ? kp : INT32_MAX);
+                const int kmax = all ? 0 : __reduce_max_sync(kAll, mine ? kp : INT32_MIN);
                 float sum = 0.f;
                 for (int c = 0; c < chunks; ++c) {
                     if (!resident) {
-                        named_bar_sync(bar_group, 256);
+                        named_bar_sync(bar_group, 128);
                         fetch(c);
-                        named_bar_sync(bar_group, 256);
+                        named_bar_sync(bar_group, 128);
                     }
                     if (seg.skip(j, c)) continue;
-                    const int buf = cnt & 1, rows = seg.rows(c);
+                    const int rows = seg.rows(c);
                     const float *ls = lse_sh + (c % kQSlots) * kRows;
                     const int *ps = pos_sh + (c % kQSlots) * kRows;
                     const int first = s.m - s.nq + c * p.chunk_q, last = first + rows / p.group - 1;
-                    // whether every row sees every key of the warp
-                    const bool all = (old || kmax <= first) && (p.window == INT32_MAX || (int64_t)last - kmin < p.window);
-                    if (!__all_sync(kAll, wait_phase(bar(B_SFULL + 2 * x + buf), (cnt >> 1) & 1, lim, abort_flag))) {
+                    const bool open = all || ((old || kmax <= first) && (p.window == INT32_MAX || (int64_t)last - kmin < p.window));
+                    if (!__all_sync(kAll, wait_phase(bar(B_SFULL + grp), cnt & 1, lim, abort_flag))) {
                         fail(106);
                         ok = false;
                     }
                     ++cnt;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c0 = 32 * half; c0 < rows; c0 += 64) {
+                    for (int c0 = 0; c0 < rows; c0 += 32) {
                         float v[32];
-                        tmem_ld32(sa + buf * kRows + c0, v);
+                        tmem_ld32(sa + c0, v);
+                        if (c0 + 32 >= rows) {   // the last of them: the columns may be written again
+                            tc_fence_before();
+                            mbar_arrive(bar(B_SEMPTY + grp));
+                            if (c0 + 32 > rows)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = c0 + i < rows ? v[i] : 0.f;   // lse is infinite there
+                        }
                         float a[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (all && c0 + 32 <= rows) {
+                        if (open) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) {
                                 const float4 l4 = *reinterpret_cast<const float4 *>(ls + c0 + i);
@@ -430,24 +454,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 const float e = ex2_approx(fmaf(v[i], c2, -ls[c0 + i]));
-                                const bool sees = c0 + i < rows && (uint32_t)(ps[c0 + i] - kp) < (uint32_t)p.window;
-                                a[i & 3] += sees ? e : 0.f;
+                                a[i & 3] += (uint32_t)(ps[c0 + i] - kp) < (uint32_t)p.window ? e : 0.f;
                             }
                         }
                         sum += (a[0] + a[1]) + (a[2] + a[3]);
                     }
-                    tc_fence_before();
-                    mbar_arrive(bar(B_SEMPTY + 2 * x + buf));
                 }
-                if (half == 1) xch[r] = sum;
-                named_bar_sync(bar_pair, 64);
-                if (half == 0 && mine && ok) {
-                    sum += xch[r];
+                if (mine && ok) {
                     if (old) p.w_out[slot] = before + sum;
                     else p.w_new[(s.t0 + key) * p.Hkv + seg.h] = sum;
                 }
-                named_bar_sync(bar_pair, 64);
             }
+            blocks += seg.blk1 - seg.blk0;
         }
     }
     }
