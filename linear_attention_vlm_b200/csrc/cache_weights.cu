@@ -108,10 +108,15 @@ struct Walk {
                 s = load_seq(p, ++b);
             }
             const int64_t head = (int64_t)s.blocks * s.cost, off = w - base;
-            h = (int)(off / head);
+            h = head <= INT32_MAX && off <= INT32_MAX ? (int)((uint32_t)off / (uint32_t)head) : (int)(off / head);
             const int64_t at = off - h * head, upto = min(head, at + (end - w));
-            blk0 = (int)((at + s.cost - 1) / s.cost);
-            blk1 = (int)((upto + s.cost - 1) / s.cost);
+            if (s.cost == 1) {
+                blk0 = (int)at;
+                blk1 = (int)upto;
+            } else {
+                blk0 = (int)((at + s.cost - 1) / s.cost);
+                blk1 = (int)((upto + s.cost - 1) / s.cost);
+            }
             w += upto - at;
             if (blk0 < blk1) return true;
         }
@@ -188,10 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kThreads / 32; ++i) W += wsum[i];
     }
     auto my_run = [&] {
-        w0 = W * cta / gridDim.x;
-        w1 = W * (cta + 1) / gridDim.x;
+        const Cut cut(W, gridDim.x);
+        w0 = cut.start(cta);
+        w1 = cut.start(cta + 1);
     };
-    my_run();
+    if (!one_pass) my_run();
     int64_t carry = 0;
     for (int b0 = 0; b0 < p.num_seqs && carry <= w0; b0 += kThreads) {
         const int b = b0 + tid;

@@ -74,6 +74,23 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Work of W units cut evenly over N CTAs: CTA c takes [start(c), start(c + 1)),
+// where start(c) = floor(c W / N), with one wide division.
+struct Cut {
+    int64_t whole;
+    int rest, n;
+    __device__ __forceinline__ Cut(int64_t W, int N) : n(N) {
+        if (W <= INT32_MAX) {
+            whole = (uint32_t)W / (uint32_t)N;
+            rest = (int)((uint32_t)W % (uint32_t)N);
+        } else {
+            whole = W / N;
+            rest = (int)(W % N);
+        }
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return whole * c + rest * c / n; }   // n, c < 2^15
+};
+
 // Parent of node i (of a tree whose first row is bos): -1, or an index below
 // i; anything else is read as -1.  Without a table the tree is a chain.
 __device__ __forceinline__ int tree_parent(const int32_t *parents, int64_t bos, int i) {

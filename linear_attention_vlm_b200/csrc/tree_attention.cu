@@ -219,9 +219,6 @@ template <bool ROWS> struct Halves {
     __device__ __forceinline__ bool done(const Walk<ROWS> &seg) const { return j >= seg.blk1; }
 };
 
-// CTA c of N takes units [c W / N, (c + 1) W / N); with N <= W no run is empty.
-__device__ __forceinline__ int64_t run_start(int64_t W, int c, int N) { return W * c / N; }
-
 template <bool ROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mKc,
@@ -294,11 +291,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kThreads / 32; ++i) W += wsum[i];
     }
     auto my_run = [&] {
-        const int runs = (int)min((int64_t)gridDim.x, W);
-        w0 = cta < runs ? run_start(W, cta, runs) : W;
-        w1 = cta < runs ? run_start(W, cta + 1, runs) : W;
+        const int runs = (int)min((int64_t)gridDim.x, W);   // no run is empty
+        w0 = w1 = W;
+        if (cta < runs) {
+            const Cut cut(W, runs);
+            w0 = cut.start(cta);
+            w1 = cut.start(cta + 1);
+        }
     };
-    my_run();
+    if (!one_pass) my_run();
     int64_t carry = 0;
     for (int b0 = 0; b0 < p.num_seqs && (carry <= w0 || cta == 0); b0 += kThreads) {
         const int b = b0 + tid;
