@@ -418,6 +418,17 @@ def test_insert_row_sizes(dtype, d):
     run_insert([50, 20], [9, 70], 50, 3, 5, d, dtype=dtype, d=d)
 
 
+@pytest.mark.parametrize("Hkv", [5, 7, 8, 9, 16])
+@pytest.mark.parametrize("ms,in_place", [([1, 0, 9], True), ([200, 3, 1], False), ([6] * 40, True)])
+def test_insert_heads_and_lists(Hkv, ms, in_place):
+    # few rows a head, many rows a head, more lists than SMs
+    run_insert([100 - i % 3 for i in range(len(ms))], ms, 100, Hkv, 20, Hkv, d=64, in_place=in_place)
+
+
+def test_insert_many_rows_of_many_lists():
+    run_insert([70] * 75, [30 + 5 * (i % 9) for i in range(75)], 70, 1, 10, 4)
+
+
 def odd_weights(r, shape):
     """Many ties, zeros of both signs, negatives, infinities and NaN."""
     return r.choice(np.array([0.0, -0.0, 1.0, 1.0, -2.0, np.inf, -np.inf, np.nan, 1e-40, 3e38], np.float32), shape)
