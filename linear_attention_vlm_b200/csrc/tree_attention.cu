@@ -21,7 +21,9 @@
 //   by keys (trees of at most one tile): stream x takes half x of every block
 //     for the same rows, and the streams are merged at the end;
 //   by rows (larger trees): the streams take two row tiles of the same half
-//     block, so a block is loaded once for 256 rows.
+//     block, so a block is loaded once for 256 rows.  For a tree of one tile the
+//     second stream would idle: 70 against 57 us for a token of 64 sequences
+//     at 0 to 8192 slots, 53 against 48 for 32 trees of 16 nodes.
 // With two buffers the scores of the next half are formed while the softmax of
 // this one runs, so the softmax warps hardly wait; a thread holds a whole row of
 // 64 scores in registers, so a row needs no exchange and its scores are read once.
@@ -30,6 +32,13 @@
 //   warps 9, 10       MMA issuers of stream 0 / 1: with one warp for both, its
 //                     waits and issues (about 3000 cycles per half block) were
 //                     longer than the products and the softmax (1200 each)
+// Bandwidth and rates reached, bf16, 16 query and 2 key/value heads: a token of 64
+// sequences at 0 to 8192 slots 57 us (4.6 TB/s, of which 13 us are the first
+// copies, the merge and the join); 24 nodes at 262144 slots 83 us (3.2 TB/s, 0.6
+// PFLOP/s); 32 trees of 64 nodes at 8192 slots 167 us.  With many rows the hand-over
+// between softmax and products of a stream bounds it: a half block takes 2050
+// cycles, 1350 of them the exponentials and the conversions of 128 rows x 64 keys
+// a stream (the special-function units alone need 1100 for two streams).
 // Tensor memory: per stream 2 x 64 columns of scores and 128 of output; the bf16
 // P of a half block lies over the columns of its S, read by then.
 #include <cuda.h>
@@ -58,8 +67,11 @@ constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 32 * 11;
 constexpr int kSub = 64;                // keys of a half block
 // Planning weight of an item beside its key blocks: starting one (its Q, the
-// first scores) and ending it (merge and stores) take about a block's time.
-constexpr int kItemCost = 1;
+// first scores) and ending it (merge and stores) take the time of one or two
+// blocks.  Weights 0, 1 and 2: 50.1, 48.8, 46.7 us for 32 trees of 16 nodes at
+// 8192 slots of 2 x 8 heads, 112, 107, 105 of 64 nodes, 58.7, 56.9, 58.1 for a
+// token of 64 sequences, 60.1, 60.5, 58.8 for one of 512 at 100 slots.
+constexpr int kItemCost = 2;
 
 // shared memory: [Q tiles][K ring][V ring][barriers][exchange]
 template <bool ROWS> struct Cfg {
@@ -886,7 +898,8 @@ template <bool ROWS> cudaError_t launch(const TreeAttnLaunch &L, cudaStream_t st
     p.ml = reinterpret_cast<float2 *>(ws + w.ml);
     p.part = reinterpret_cast<float *>(ws + w.part);
     p.timeout_ns = L.timeout_ns; p.drain_ns = L.drain_ns;
-    // trees of at most half a tile leave room for the next item's Q beside this one's
+    // trees of at most half a tile leave room for the next item's Q beside this
+    // one's (a token of 64 sequences: 56.9 against 58.3 us)
     p.box_nodes = ROWS ? nodes : L.max_nodes;
     p.q_bufs = !ROWS && group * L.max_nodes <= kBM / 2 ? 2 : 1;
     CUtensorMap mq, mkc, mvc, mkn, mvn;
@@ -903,7 +916,9 @@ template <bool ROWS> cudaError_t launch(const TreeAttnLaunch &L, cudaStream_t st
     tree_attention_kernel<ROWS><<<ctas, kThreads, Cfg<ROWS>::kSmem, stream>>>(mq, mkc, mvc, mkn, mvn, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // few items are cut many times: then a whole block joins a row
+    // Few items are cut many times: then a whole block joins a row.  A warp and a
+    // block a row: 30.7 and 16.5 us for one token at 8192 slots, 108 and 83 for 24
+    // nodes at 262144; 169 and 270 for 32 trees of 64 nodes, of two parts each.
     const int64_t items = (int64_t)L.num_seqs * L.Hkv * (ROWS ? ((L.max_nodes + nodes - 1) / nodes + 1) / 2 : 1);
     const int width = items * 8 <= ctas ? kJoinWarps : 1;
     const int64_t per = kJoinWarps / width, blocks = ((int64_t)L.max_nodes * L.Hq + per - 1) / per;

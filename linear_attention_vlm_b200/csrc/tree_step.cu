@@ -19,6 +19,10 @@
 // A fragments of the second product, with M: nothing of size n x d leaves the
 // registers between them.  tcgen05 would want S as bf16 pairs in shared memory
 // and twice the passes through it for products this small (n <= 64 columns).
+// With d = 128 in bf16, 64 sequences of 16 heads (67 MB of state) take 19.1 us
+// at 4 nodes and 21.5 at 16 (3.7 TB/s with the rows); at 64 nodes 80.6, where
+// the chain of the substitution (64 steps in two warps) and the products that
+// wait for it take the time.  One sequence of 7 nodes takes 4.3, a launch's latency.
 //
 // Precision: with bf16 inputs S, R and M enter as hi + lo bf16 pairs (2^-17
 // relative, far below the rounding of the output); with fp32 inputs every
@@ -186,8 +190,14 @@ template <typename T, int D, int NP> struct Shape {
                             kn = kp + NP * kP * 4, kBytes = kn + NP * (4 + 4 + 8 + 4);
 };
 
+// CTAs of an SM.  Two hide one another's phases, which outweighs the spills that
+// their registers cost (64 sequences of 16 heads, d = 128, bf16: 47.1 -> 36.4 us
+// at 32 nodes, 94.0 -> 80.6 at 64; fp32 87 -> 73 at 32), except where every
+// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two.
+template <typename T, int D, int NP> constexpr int kPerSm = sizeof(T) == 4 && D == 128 && NP == 64 ? 1 : 2;
+
 template <typename T, int D, int NP>
-__global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, NP <= 16 ? 2 : 1)
+__global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
     tree_step_kernel(const TreeStepLaunch L, int64_t uniform_len) {
     using S = Shape<T, D, NP>;
     using F = Frag<T>;
@@ -424,7 +434,9 @@ template <typename T, int D, int NP> cudaError_t launch(const TreeStepLaunch &L,
 }
 
 // The node count fixes the registers that hold S k, S q and a row of M, so it
-// is a compile-time bound: 16, 32 or 64.
+// is a compile-time bound: 16, 32 or 64.  At 16 nodes (64 sequences of 16
+// heads, d = 128, bf16) the bounds of 16 and 32 take 21.5 and 29.9 us; at 32
+// nodes those of 32 and 64 take 36.4 and 71.6.
 template <typename T, int D> cudaError_t launch_nodes(const TreeStepLaunch &L, cudaStream_t stream) {
     if (L.max_nodes <= 16) return launch<T, D, 16>(L, stream);
     if (L.max_nodes <= 32) return launch<T, D, 32>(L, stream);
