@@ -20,7 +20,7 @@
 // registers between them.  tcgen05 would want S as bf16 pairs in shared memory
 // and twice the passes through it for products this small (n <= 64 columns).
 // With d = 128 in bf16, 64 sequences of 16 heads (67 MB of state) take 19.1 us
-// at 4 nodes and 21.5 at 16 (3.7 TB/s with the rows); at 64 nodes 80.6, where
+// at 4 nodes and 21.5 at 16 (3.7 TB/s with the rows); at 64 nodes 77.5, where
 // the chain of the substitution (64 steps in two warps) and the products that
 // wait for it take the time.  One sequence of 7 nodes takes 4.3, a launch's latency.
 //
@@ -193,7 +193,7 @@ template <typename T, int D, int NP> struct Shape {
 // CTAs of an SM.  Two hide one another's phases, which outweighs the spills that
 // their registers cost (64 sequences of 16 heads, d = 128, bf16: 47.1 -> 36.4 us
 // at 32 nodes, 94.0 -> 80.6 at 64; fp32 87 -> 73 at 32), except where every
-// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two.
+// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two (162 now).
 template <typename T, int D, int NP> constexpr int kPerSm = sizeof(T) == 4 && D == 128 && NP == 64 ? 1 : 2;
 
 template <typename T, int D, int NP>
@@ -287,15 +287,18 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
     // A and P: products of keys and queries with keys, decayed, 0 where j is no ancestor
     const int tiles = (n + 7) / 8;   // 8 nodes each
     {
-        // tiles of 16 rows (keys, then queries) by 8 keys, dealt to all warps
-        constexpr int MT = NP / 16, JT = NP / 8;
+        // tiles of 16 rows (keys, then queries) by 8 keys, dealt to all warps; as
+        // ancestors come before, row block r has 2 (r + 1) of them and nothing
+        // reads what lies to their right
+        constexpr int MT = NP / 16;
+        const int nb = MT == 1 ? 1 : (n + 15) / 16, of_keys = nb * (nb + 1);
 #pragma unroll 1
-        for (int w = warp; w < 2 * MT * JT; w += S::kThreads / 32) {
-            const int mt = w / JT, j0 = w % JT * 8, i0 = mt % MT * 16;
-            const bool reads = mt >= MT;                            // a tile of queries
-            if (i0 >= n) continue;
+        for (int w = warp; w < 2 * of_keys; w += S::kThreads / 32) {
+            const bool reads = w >= of_keys;                        // a tile of queries
+            const int u = reads ? w - of_keys : w, r = MT == 1 ? 0 : (u >= 2) + (u >= 6) + (u >= 12);
+            const int i0 = 16 * r, j0 = 8 * (u - r * (r + 1)), mt = r + (reads ? MT : 0);
             float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            if (j0 < i0 + 16) {                                    // ancestors come before
+            {
                 const T *r0 = kq + (mt * 16 + g) * S::kRow + 4 * t, *r1 = r0 + 8 * S::kRow;
                 const T *rb = kq + (j0 + g) * S::kRow + 4 * t;
 #pragma unroll
@@ -307,12 +310,12 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
             }
             const float2 Gj = *reinterpret_cast<const float2 *>(Gs + j0 + 2 * t);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int i = i0 + g + 8 * r, j = j0 + 2 * t;
+            for (int e = 0; e < 2; ++e) {
+                const int i = i0 + g + 8 * e, j = j0 + 2 * t;
                 const unsigned two = (unsigned)(anc[i] >> j) & 3u;
                 const float G = Gs[i];
-                float x = two & 1 ? (c[0][2 * r] + c[1][2 * r]) * F::exp(G - Gj.x) : 0.f;
-                float y = two & 2 ? (c[0][2 * r + 1] + c[1][2 * r + 1]) * F::exp(G - Gj.y) : 0.f;
+                float x = two & 1 ? (c[0][2 * e] + c[1][2 * e]) * F::exp(G - Gj.x) : 0.f;
+                float y = two & 2 ? (c[0][2 * e + 1] + c[1][2 * e + 1]) * F::exp(G - Gj.y) : 0.f;
                 if (!reads) {
                     const float be = bs[i];
                     x = j == i ? 0.f : x * be;
@@ -329,25 +332,32 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
         const int i = tid - 32 * S::kMain;
         if (i < NP) {
             float m[NP];
+            // steps without a branch between them, so that the loads of the next run
+            // ahead: 15.8 -> 12.9 us for 24 fp32 trees of 33 nodes; at 32 nodes the
+            // registers this takes cost 2 %
+            constexpr int kRun = NP == 64 ? 16 : 1;
             float *row = ps + i * S::kP;
 #pragma unroll
             for (int j = 0; j < NP; j += 4) {
-                const float4 v = i < n ? *reinterpret_cast<const float4 *>(row + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 v = i < n && (NP == 16 || j <= (i | 15)) ? *reinterpret_cast<const float4 *>(row + j) : make_float4(0.f, 0.f, 0.f, 0.f);
                 m[j] = v.x;
                 m[j + 1] = v.y;
                 m[j + 2] = v.z;
                 m[j + 3] = v.w;
             }
 #pragma unroll
-            for (int l = NP - 1; l > 0; --l) {
-                if (l < n) {
+            for (int l0 = NP - kRun; l0 >= 0; l0 -= kRun) {
+                if (l0 < n) {
 #pragma unroll
-                    for (int j = 0; j < l; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(as + l * S::kA + j);
-                        m[j] = fmaf(-m[l], a.x, m[j]);
-                        if (j + 1 < l) m[j + 1] = fmaf(-m[l], a.y, m[j + 1]);
-                        if (j + 2 < l) m[j + 2] = fmaf(-m[l], a.z, m[j + 2]);
-                        if (j + 3 < l) m[j + 3] = fmaf(-m[l], a.w, m[j + 3]);
+                    for (int l = l0 + kRun - 1; l >= max(l0, 1); --l) {
+#pragma unroll
+                        for (int j = 0; j < l; j += 4) {
+                            const float4 a = *reinterpret_cast<const float4 *>(as + l * S::kA + j);
+                            m[j] = fmaf(-m[l], a.x, m[j]);
+                            if (j + 1 < l) m[j + 1] = fmaf(-m[l], a.y, m[j + 1]);
+                            if (j + 2 < l) m[j + 2] = fmaf(-m[l], a.z, m[j + 2]);
+                            if (j + 3 < l) m[j + 3] = fmaf(-m[l], a.w, m[j + 3]);
+                        }
                     }
                 }
             }
