@@ -187,8 +187,9 @@ const char *gdn_status_string(int status);
  * kernel then records a nonzero code in a device int32 and returns, leaving
  * its outputs invalid but the GPU usable.  The word is the first int32 of the
  * workspace of gdn_prefill (and of a session's workspace; cleared by every
- * call that uses the tensor-core path) and the `status` argument of
- * gdn_swa_attention (cleared by the caller).
+ * call that uses the tensor-core path), of gdn_tree_attention and of
+ * gdn_cache_weights (set by every call that launches), and the `status`
+ * argument of gdn_swa_attention (cleared by the caller).
  *
  * gdn_read_status waits for `stream`, then reads the int32 at `word` (device,
  * 4-byte aligned): GDN_OK if it is 0, GDN_ERR_TIMEOUT otherwise; *code (may
@@ -200,7 +201,8 @@ int gdn_read_status(const int32_t *word, void *stream, int32_t *code);
  * Test hook of those bounded waits.  Sets, for the calling host thread, the
  * bound on the waits of the work loops of the tensor-core kernels that its
  * later calls launch (gdn_prefill, gdn_prefill_noalloc, gdn_swa_attention,
- * and the prefill steps a session captures).  With ns = 0 a wait gives up as
+ * gdn_tree_attention, gdn_cache_weights, and the prefill steps a session
+ * captures).  With ns = 0 a wait gives up as
  * soon as the phase it waits for is not already complete, so a call's first
  * wait on a copy or an MMA in flight gives up; GDN_WAIT_LIMIT_DEFAULT
  * restores the 2 s default.  Whatever the bound, the waits that drain a
@@ -397,7 +399,13 @@ int gdn_swa_attention(const void *q, const void *k, const void *v, void *o, cons
  * position s and seen[b] is cache_lens[b].
  *
  * cu_seqlens is as in gdn_prefill throughout (NULL: equal sequences); rows
- * from cu_seqlens[num_seqs] on are neither read nor written.
+ * from cu_seqlens[num_seqs] on are neither read nor written.  Of a sequence
+ * with more than max_nodes nodes the first max_nodes count and the others'
+ * rows are left as they are.
+ *
+ * The calls keep nothing from one to the next, so all can be captured into a
+ * CUDA graph and replayed.  Calls whose work may overlap on the GPU (other
+ * streams, a graph replayed beside them) need a workspace each.
  */
 
 /* Most nodes of one sequence's tree. */
@@ -460,8 +468,10 @@ int gdn_tree_attention(const void *q, const void *k, const void *v, const int32_
  *   out     [total_nodes, H, dv]  dtype (written; may not overlap the inputs)
  *   max_nodes  1 .. GDN_MAX_TREE_NODES: no sequence has more nodes
  * The state enters the products in fp32 (GDN_F32) or as the sum of two bf16
- * numbers (GDN_BF16, relative error 2^-17).  Supported: dk = dv in {64, 128};
- * dtype GDN_F32 or GDN_BF16.
+ * numbers (GDN_BF16, relative error 2^-17).  The nodes of a sequence are
+ * solved for together, so a value that is not finite in one of them reaches
+ * the others of its sequence (and no other sequence).  Supported: dk = dv in
+ * {64, 128}; dtype GDN_F32 or GDN_BF16.
  */
 int gdn_tree_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
                   const int32_t *parents, const float *state, void *out, const int32_t *cu_seqlens, int num_seqs,

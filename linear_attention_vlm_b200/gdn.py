@@ -708,6 +708,11 @@ def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cac
     return weights_out, new_weights
 
 
+def gdn_cache_insert_workspace_size(num_seqs: int, total_tokens: int, capacity: int, Hkv: int, d: int = 128,
+                                    dtype: torch.dtype = torch.bfloat16) -> int:
+    return _cache_insert_ws(num_seqs, total_tokens, capacity, Hkv, d, _dtype_code(dtype))
+
+
 def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      weights: torch.Tensor, cache_pos: torch.Tensor, cache_lens: torch.Tensor, seen: torch.Tensor,
                      cu_seqlens: Optional[torch.Tensor] = None, *, recent: int = 0,
