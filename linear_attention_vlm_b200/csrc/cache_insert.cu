@@ -297,11 +297,14 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
     sync_all();
     // A new token that stays: its slot, weight and position.  (Where cu_seqlens
     // decreases, sequences share tokens and may find one another's ranks.)
-    auto place = [&](int r) { return (unsigned)r < (unsigned)m && (unsigned)places[r] < (unsigned)cap ? places[r] : -1; };
     auto settle = [&](int64_t j) -> int {
         int32_t *slot = L.slots + (t0 + j) * L.Hkv + h;
-        const int s = place(*slot);
-        if (s < 0) return -1;
+        const int r = *slot;
+        const int s = (unsigned)r < (unsigned)m ? places[r] : -1;
+        if ((unsigned)s >= (unsigned)cap) {
+            if (r >= 0) *slot = -1;
+            return -1;
+        }
         *slot = s;
         L.w_out[base + s] = new_weight((int)j);
         L.pos_out[base + s] = (int32_t)(seen + j);
@@ -320,11 +323,14 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheIn
                 w[e] = at < m ? new_weight((int)at) : 0.f;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = place(r[e]);
+            for (int e = 0; e < 4; ++e) s[e] = (unsigned)r[e] < (unsigned)m ? places[r[e]] : -1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (s[e] < 0) continue;
                 const int64_t at = j + e * all_threads;
+                if ((unsigned)s[e] >= (unsigned)cap) {
+                    if (r[e] >= 0) L.slots[(t0 + at) * L.Hkv + h] = -1;
+                    continue;
+                }
                 L.slots[(t0 + at) * L.Hkv + h] = s[e];
                 L.w_out[base + s[e]] = w[e];
                 L.pos_out[base + s[e]] = (int32_t)(seen + at);
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kCopyWarps * 32) cache_copy_kernel(const Cache
     for (int64_t r = (int64_t)blockIdx.x * kCopyWarps + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * kCopyWarps) {
         const int64_t at = t0 * L.Hkv + r;
         const int s = L.slots[at], h = (int)(r % L.Hkv);
-        if ((unsigned)s >= (unsigned)L.capacity) continue;   // -1: did not stay
+        if (s < 0) continue;
         const int64_t to = ((int64_t)b * L.capacity + s) * L.Hkv + h;
         for (int64_t x = lane; x < 2 * vecs; x += 32) {
             const bool value = x >= vecs;
