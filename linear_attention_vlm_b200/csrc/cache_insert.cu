@@ -17,7 +17,7 @@
 // the keys, each a barrier apart: 19 us for 8192 slots, of which the bytes take
 // 3, for one list and for 128 alike.  A (sequence, head) with more candidates
 // than one CTA keeps is spread over a cluster of CTAs that read one another's
-// histograms: 33 against 79 us for 40960 candidates.  With fewer the barriers
+// histograms: 34 against 79 us for 40960 candidates.  With fewer the barriers
 // of a cluster cost more than the shared work gives (23 against 19.5 us, 8193
 // candidates over 4 CTAs).
 #include <cooperative_groups.h>
