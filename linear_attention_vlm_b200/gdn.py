@@ -598,8 +598,14 @@ def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent
     n = _tree_nodes(max_nodes, cu_seqlens, T, B)
     if out is None:
         out = torch.empty_like(q)
+        o_at = out.data_ptr()
+    else:
+        o_at = _arg("out", out, q.shape, dt, dev)
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _arg("lse", lse, (T, Hq), torch.float32, dev)
     code = _dtype_code(dt)
     ws, ws_bytes = _scratch(workspace, _tree_attention_ws(B, T, n, cap, Hq, Hkv, d, code), dev)
     i32, new, old = torch.int32, (T, Hkv, d), (B, cap, Hkv, d)
@@ -609,7 +615,7 @@ def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent
         _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), _arg("k_cache", k_cache, old, dt, dev),
         _arg("v_cache", v_cache, old, dt, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
         _opt("cache_pos", cache_pos, (B, Hkv, cap), i32, dev), _opt("seen", seen, (B,), i32, dev),
-        _arg("out", out, q.shape, dt, dev), _arg("lse", lse, (T, Hq), torch.float32, dev), B, T, n, cap, Hq, Hkv, d,
+        o_at, lse_at, B, T, n, cap, Hq, Hkv, d,
         int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
         _stream(dev))
     guard = _current(dev)
@@ -637,14 +643,17 @@ def gdn_tree_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
         raise ValueError("gdn_tree_step needs CUDA tensors")
     B = state.shape[0]
     n = _tree_nodes(max_nodes, cu_seqlens, T, B)
+    i32, f32, rows = torch.int32, torch.float32, (T, H, d)
     if out is None:
         out = torch.empty_like(v)
-    i32, f32, rows = torch.int32, torch.float32, (T, H, d)
+        o_at = out.data_ptr()
+    else:
+        o_at = _arg("out", out, rows, dt, dev)
     args = (
         _arg("q", q, rows, dt, dev), _arg("k", k, rows, dt, dev),
         _arg("v", v, rows, dt, dev), _arg("g", g, (T, H), f32, dev), _arg("beta", beta, (T, H), f32, dev),
         _opt("parents", parents, (T,), i32, dev), _arg("state", state, (B, H, d, d), f32, dev),
-        _arg("out", out, rows, dt, dev), _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, n, H, d, d,
+        o_at, _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, n, H, d, d,
         _dtype_code(dt),
         _stream(dev))
     guard = _current(dev)
@@ -681,18 +690,20 @@ def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cac
     if dev.type != "cuda":
         raise ValueError("gdn_cache_weights needs CUDA tensors")
     B, cap, Hkv = k_cache.shape[:3]
-    if weights_out is None:
-        weights_out = weights
     if new_weights is None:
         new_weights = torch.empty((T, Hkv), dtype=torch.float32, device=dev)
+        new_at = new_weights.data_ptr()
+    else:
+        new_at = _arg("new_weights", new_weights, (T, Hkv), torch.float32, dev)
     code = _dtype_code(dt)
     ws, ws_bytes = _scratch(workspace, _cache_weights_ws(B, Tq, T, cap, Hq, Hkv, d, code), dev)
     i32, f32, cells = torch.int32, torch.float32, (B, Hkv, cap)
+    w_at = _arg("weights", weights, cells, f32, dev)
     args = (
         _arg("q", q, q.shape, dt, dev), _arg("lse", lse, (Tq, Hq), f32, dev),
         _arg("k", k, (T, Hkv, d), dt, dev), _arg("k_cache", k_cache, (B, cap, Hkv, d), dt, dev),
-        _arg("weights", weights, cells, f32, dev), _arg("weights_out", weights_out, cells, f32, dev),
-        _arg("new_weights", new_weights, (T, Hkv), f32, dev), _opt("cu_queries", cu_queries, (B + 1,), i32, dev),
+        w_at, w_at if weights_out is None else _arg("weights_out", weights_out, cells, f32, dev),
+        new_at, _opt("cu_queries", cu_queries, (B + 1,), i32, dev),
         _opt("cu_tokens", cu_tokens, (B + 1,), i32, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
         _opt("cache_pos", cache_pos, cells, i32, dev), _opt("seen", seen, (B,), i32, dev), B, Tq, T, cap, Hq, Hkv, d,
         int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
@@ -705,7 +716,7 @@ def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cac
             st = _load().gdn_cache_weights(*args)
     if st != GDN_OK:
         raise GdnError(st, "gdn_cache_weights")
-    return weights_out, new_weights
+    return weights if weights_out is None else weights_out, new_weights
 
 
 def gdn_cache_insert_workspace_size(num_seqs: int, total_tokens: int, capacity: int, Hkv: int, d: int = 128,
@@ -733,6 +744,9 @@ def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
     B, cap = k_cache.shape[:2]
     if slots is None:
         slots = torch.empty((T, Hkv), dtype=torch.int32, device=dev)
+        slots_at = slots.data_ptr()
+    else:
+        slots_at = _arg("slots", slots, (T, Hkv), torch.int32, dev)
     code = _dtype_code(dt)
     ws, ws_bytes = _scratch(workspace, _cache_insert_ws(B, T, cap, Hkv, d, code), dev)
     i32, f32, rows, cells = torch.int32, torch.float32, (T, Hkv, d), (B, Hkv, cap)
@@ -745,7 +759,7 @@ def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
         p, p if pos_out is None else _arg("pos_out", pos_out, cells, i32, dev),
         ln, ln if lens_out is None else _arg("lens_out", lens_out, (B,), i32, dev),
         sn, sn if seen_out is None else _arg("seen_out", seen_out, (B,), i32, dev),
-        _opt("new_weights", new_weights, (T, Hkv), f32, dev), _arg("slots", slots, (T, Hkv), i32, dev),
+        _opt("new_weights", new_weights, (T, Hkv), f32, dev), slots_at,
         _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, cap, Hkv, d, int(recent), code, ws.data_ptr(),
         ws_bytes,
         _stream(dev))
