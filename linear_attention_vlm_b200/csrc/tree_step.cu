@@ -26,7 +26,8 @@
 //
 // Precision: with bf16 inputs S, R and M enter as hi + lo bf16 pairs (2^-17
 // relative, far below the rounding of the output); with fp32 inputs every
-// operand is split into two tf32 numbers and three products are taken (2^-21).
+// operand is split into two tf32 numbers and three products are taken (2^-22);
+// the errors are then those of a plain fp32 evaluation (1.5e-7 in the norm).
 // All sums are fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,10 +72,11 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
     lo = pack2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
 }
 
-// hi + lo = x up to 2^-21: 11 significant bits each, cut and then rounded by the unit
+// hi + lo = x up to 2^-23: 11 significant bits each, rounded to nearest; of lo
+// the unit drops what lies below.  (cvt.rna.tf32 rounds alike and took a quarter more time.)
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
 
 // The product fragments of 16 channels.  An A fragment holds two rows (lane
@@ -146,13 +148,20 @@ template <> struct Frag<float> {
         split_tf32(v.z, b.hi[2], b.lo[2]);
         split_tf32(v.w, b.hi[3], b.lo[3]);
     }
+    // The unit cuts its sums, always towards zero, so a long sum in it drifts
+    // (1e-6 over 128 channels).  It gets 16 channels at a time, the small products
+    // first, and what it has is added here, rounded.
     __device__ static void mma(float (&c)[4], const A &a, const B &b) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            mma_tf32(c, a.lo[s], b.hi[2 * s], b.hi[2 * s + 1]);
-            mma_tf32(c, a.hi[s], b.lo[2 * s], b.lo[2 * s + 1]);
-            mma_tf32(c, a.hi[s], b.hi[2 * s], b.hi[2 * s + 1]);
+            mma_tf32(x, a.lo[s], b.hi[2 * s], b.hi[2 * s + 1]);
+            mma_tf32(x, a.hi[s], b.lo[2 * s], b.lo[2 * s + 1]);
         }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) mma_tf32(x, a.hi[s], b.hi[2 * s], b.hi[2 * s + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] += x[e];
     }
     __device__ static void mma_rows(float (&c)[4], const float *r0, const float *r1, const B &b) {
         A a;
@@ -162,19 +171,23 @@ template <> struct Frag<float> {
     __device__ static void mma_nodes(float (&c)[4], const float (&x)[4], const float (&y)[4], const float2 &m0, const float2 &m1) {
         const float *src[2] = {x, y};
         const float2 ms[2] = {m0, m1};
+        uint32_t hi[2][4], lo[2][4], mh[2][2], ml[2][2];   // nodes 2t, 2t + 1 as the k indices t, t + 4
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            uint32_t hi[4], lo[4], mh[2], ml[2];   // nodes 2t, 2t + 1 as the k indices t, t + 4
-            split_tf32(src[s][0], hi[0], lo[0]);
-            split_tf32(src[s][2], hi[1], lo[1]);
-            split_tf32(src[s][1], hi[2], lo[2]);
-            split_tf32(src[s][3], hi[3], lo[3]);
-            split_tf32(ms[s].x, mh[0], ml[0]);
-            split_tf32(ms[s].y, mh[1], ml[1]);
-            mma_tf32(c, lo, mh[0], mh[1]);
-            mma_tf32(c, hi, ml[0], ml[1]);
-            mma_tf32(c, hi, mh[0], mh[1]);
+            split_tf32(src[s][0], hi[s][0], lo[s][0]);
+            split_tf32(src[s][2], hi[s][1], lo[s][1]);
+            split_tf32(src[s][1], hi[s][2], lo[s][2]);
+            split_tf32(src[s][3], hi[s][3], lo[s][3]);
+            split_tf32(ms[s].x, mh[s][0], ml[s][0]);
+            split_tf32(ms[s].y, mh[s][1], ml[s][1]);
+            mma_tf32(d, lo[s], mh[s][0], mh[s][1]);
+            mma_tf32(d, hi[s], ml[s][0], ml[s][1]);
         }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) mma_tf32(d, hi[s], mh[s][0], mh[s][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] += d[e];
     }
 };
 
@@ -192,8 +205,8 @@ template <typename T, int D, int NP> struct Shape {
 
 // CTAs of an SM.  Two hide one another's phases, which outweighs the spills that
 // their registers cost (64 sequences of 16 heads, d = 128, bf16: 47.1 -> 36.4 us
-// at 32 nodes, 94.0 -> 80.6 at 64; fp32 87 -> 73 at 32), except where every
-// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two (162 now).
+// at 32 nodes, 94.0 -> 80.6 at 64; fp32 87 -> 73 at 32, now 82), except where every
+// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two (185 now).
 template <typename T, int D, int NP> constexpr int kPerSm = sizeof(T) == 4 && D == 128 && NP == 64 ? 1 : 2;
 
 template <typename T, int D, int NP>
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
         if (i < NP) {
             float m[NP];
             // steps without a branch between them, so that the loads of the next run
-            // ahead: 15.8 -> 12.9 us for 24 fp32 trees of 33 nodes; at 32 nodes the
+            // ahead: 15.8 -> 12.9 us for 24 fp32 trees of 33 nodes (13.2 now); at 32 nodes the
             // registers this takes cost 2 %
             constexpr int kRun = NP == 64 ? 16 : 1;
             float *row = ps + i * S::kP;

@@ -336,6 +336,23 @@ def test_step(dtype, d, nodes, kind):
         assert torch.equal(a, out[:T])
 
 
+@pytest.mark.parametrize("d,nodes", [(64, 33), (128, 1), (128, 16), (128, 64)])
+def test_step_in_fp32_is_as_exact_as_fp32(d, nodes):
+    """In the norm: operands are off by 2^-23 at most and one of four partial
+    products is left out (3 2^-22 for a product of two), sums are rounded d/16 +
+    n/8 times by half a step, with either sign (under 2^-22): below 2^-20."""
+    gen = torch.Generator().manual_seed(nodes)
+    mk = lambda *s: torch.randn(s, generator=gen)                                # noqa: E731
+    B, H = 4, 3
+    T = B * nodes
+    q, k = (torch.nn.functional.normalize(mk(T, H, d), dim=-1) for _ in range(2))
+    v, g, beta, S = mk(T, H, d), -0.2 * mk(T, H).abs(), torch.rand(T, H, generator=gen), mk(B, H, d, d)
+    parents, cu = [i // 2 - 1 for _ in range(B) for i in range(nodes)], cu_of([nodes] * B)
+    out = gdn.gdn_tree_step(*(x.to(DEV) for x in (q, k, v, g, beta)), ints(parents), S.to(DEV), ints(cu))
+    ref = D.tree_step(*(np64(x) for x in (q, k, v, g, beta)), parents, np64(S), cu)
+    assert np.linalg.norm(np64(out) - ref) <= 2.0 ** -20 * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_step_of_a_root_is_a_decode_step(dtype):
     B, H, d = 5, 4, 128
