@@ -5,8 +5,10 @@
 // M side of the tensor-core products, 128 rows a tile, node by node.  Per
 // block of 128 keys: S = Q K^T (fp32 in tensor memory), P = 2^(c S - m) with a
 // running maximum m and row sum, O += P V with P as the bf16 A operand in
-// tensor memory.  The last block of an item holds the tree's own keys, masked
-// by the ancestor bits of each node; a cache's last block ends inside the tile.
+// tensor memory (its rounding adds as much error as the output's: 2.2e-3 in the norm
+// against 1.6e-3; the row sums take the unrounded P).  The last block of an item
+// holds the tree's own keys, masked by the ancestor bits of each node; a cache's
+// last block ends inside the tile.
 //
 // What bounds it: K and V are read once, 512 bytes a slot and key/value head,
 // against 512 Hq / Hkv n flops: memory up to about n Hq / Hkv = 260 rows, the
