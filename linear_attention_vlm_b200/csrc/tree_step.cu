@@ -26,7 +26,7 @@
 //
 // Precision: with bf16 inputs S, R and M enter as hi + lo bf16 pairs (2^-17
 // relative, far below the rounding of the output); with fp32 inputs every
-// operand is split into two tf32 numbers and three products are taken (2^-22);
+// operand is split into two tf32 numbers and three products are taken (2^-21);
 // the errors are then those of a plain fp32 evaluation (1.5e-7 in the norm).
 // All sums are fp32.
 #include <cuda_bf16.h>
@@ -72,11 +72,12 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
     lo = pack2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
 }
 
-// hi + lo = x up to 2^-23: 11 significant bits each, rounded to nearest; of lo
-// the unit drops what lies below.  (cvt.rna.tf32 rounds alike and took a quarter more time.)
+// hi + lo = x up to 2^-21: 11 significant bits each, hi rounded to nearest, so
+// that lo has either sign and what the unit cuts off it does not add up.  A NaN
+// stays one in lo.  (cvt.rna.tf32 rounds alike and took a quarter more time.)
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 // The product fragments of 16 channels.  An A fragment holds two rows (lane
@@ -205,8 +206,8 @@ template <typename T, int D, int NP> struct Shape {
 
 // CTAs of an SM.  Two hide one another's phases, which outweighs the spills that
 // their registers cost (64 sequences of 16 heads, d = 128, bf16: 47.1 -> 36.4 us
-// at 32 nodes, 94.0 -> 80.6 at 64; fp32 87 -> 73 at 32, now 82), except where every
-// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two (185 now).
+// at 32 nodes, 94.0 -> 80.6 at 64; fp32 87 -> 73 at 32, now 78), except where every
+// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two (157 now).
 template <typename T, int D, int NP> constexpr int kPerSm = sizeof(T) == 4 && D == 128 && NP == 64 ? 1 : 2;
 
 template <typename T, int D, int NP>
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
         if (i < NP) {
             float m[NP];
             // steps without a branch between them, so that the loads of the next run
-            // ahead: 15.8 -> 12.9 us for 24 fp32 trees of 33 nodes (13.2 now); at 32 nodes the
+            // ahead: 15.8 -> 12.9 us for 24 fp32 trees of 33 nodes (12.6 now); at 32 nodes the
             // registers this takes cost 2 %
             constexpr int kRun = NP == 64 ? 16 : 1;
             float *row = ps + i * S::kP;

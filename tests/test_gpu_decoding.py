@@ -338,9 +338,10 @@ def test_step(dtype, d, nodes, kind):
 
 @pytest.mark.parametrize("d,nodes", [(64, 33), (128, 1), (128, 16), (128, 64)])
 def test_step_in_fp32_is_as_exact_as_fp32(d, nodes):
-    """In the norm: operands are off by 2^-23 at most and one of four partial
-    products is left out (3 2^-22 for a product of two), sums are rounded d/16 +
-    n/8 times by half a step, with either sign (under 2^-22): below 2^-20."""
+    """In the norm: operands are off by 2^-21 at most, with either sign (2^-22 in
+    the mean of their squares, two of them 2^-21.5), one of four partial products
+    is left out (2^-22), sums are rounded d/16 + n/8 times by half a step, with
+    either sign (under 2^-22): below 2^-20."""
     gen = torch.Generator().manual_seed(nodes)
     mk = lambda *s: torch.randn(s, generator=gen)                                # noqa: E731
     B, H = 4, 3
@@ -351,6 +352,23 @@ def test_step_in_fp32_is_as_exact_as_fp32(d, nodes):
     out = gdn.gdn_tree_step(*(x.to(DEV) for x in (q, k, v, g, beta)), ints(parents), S.to(DEV), ints(cu))
     ref = D.tree_step(*(np64(x) for x in (q, k, v, g, beta)), parents, np64(S), cu)
     assert np.linalg.norm(np64(out) - ref) <= 2.0 ** -20 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("what", [0, 1, 2])
+def test_step_does_not_hide_a_nan(dtype, what):
+    """A NaN of arithmetic on the device (all bits of its fraction set) in q, k
+    or v reaches the output of its node; other sequences stay as they are."""
+    gen = torch.Generator().manual_seed(what)
+    t = [(0.1 * torch.randn(6, 2, 128, generator=gen)).to(dtype).to(DEV) for _ in range(3)]
+    g, beta = -torch.rand(6, 2, generator=gen).to(DEV), torch.full((6, 2), 0.5, device=DEV)
+    S = torch.randn(2, 2, 128, 128, generator=gen).to(DEV)
+    clean = gdn.gdn_tree_step(*t, g, beta, None, S, ints([0, 3, 6]))
+    zero = torch.zeros(1, device=DEV)
+    t[what][1, 0, 5:6] = (zero / zero).to(dtype)
+    out = gdn.gdn_tree_step(*t, g, beta, None, S, ints([0, 3, 6]))
+    assert bool(out[1, 0].isnan().any())
+    assert torch.equal(out[3:], clean[3:]) and torch.equal(out[:, 1], clean[:, 1])
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
