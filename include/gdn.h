@@ -468,7 +468,10 @@ int gdn_tree_attention(const void *q, const void *k, const void *v, const int32_
  *   out     [total_nodes, H, dv]  dtype (written; may not overlap the inputs)
  *   max_nodes  1 .. GDN_MAX_TREE_NODES: no sequence has more nodes
  * The state enters the products in fp32 (GDN_F32) or as the sum of two bf16
- * numbers (GDN_BF16, relative error 2^-17).  The nodes of a sequence are
+ * numbers (GDN_BF16, relative error 2^-17).  The bound of -80 on sums of g does
+ * not hold here: sums along a path are kept to 2^-43 of their size, so gates may
+ * close as far as they like (a path sum of -2^20 leaves the decays below it off
+ * by 2^-23).  The nodes of a sequence are
  * solved for together, so a value that is not finite in one of them reaches
  * the others of its sequence (and no other sequence).  Supported: dk = dv in
  * {64, 128}; dtype GDN_F32 or GDN_BF16.

@@ -20,15 +20,17 @@
 // registers between them.  tcgen05 would want S as bf16 pairs in shared memory
 // and twice the passes through it for products this small (n <= 64 columns).
 // With d = 128 in bf16, 64 sequences of 16 heads (67 MB of state) take 19.1 us
-// at 4 nodes and 21.5 at 16 (3.7 TB/s with the rows); at 64 nodes 77.5, where
+// at 4 nodes and 21.6 at 16 (3.7 TB/s with the rows); at 64 nodes 78, where
 // the chain of the substitution (64 steps in two warps) and the products that
 // wait for it take the time.  One sequence of 7 nodes takes 4.3, a launch's latency.
 //
 // Precision: with bf16 inputs S, R and M enter as hi + lo bf16 pairs (2^-17
 // relative, far below the rounding of the output); with fp32 inputs every
 // operand is split into two tf32 numbers and three products are taken (2^-21);
-// the errors are then those of a plain fp32 evaluation (1.5e-7 in the norm).
-// All sums are fp32.
+// the errors are then those of a plain fp32 evaluation token by token (1.3e-7 to 1.9e-7
+// in the norm, whatever the gates; 1.6e-7 to 2.5e-7).  All sums are fp32, but the sums of g
+// along a path, which are pairs of fp32: a decay is the exponential of the difference
+// of two of them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -78,6 +80,15 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint3
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+// (h, l) += (x, y), each a sum of two floats that do not overlap: 2^-46 relative
+// for terms of one sign.
+__device__ __forceinline__ void add_two(float &h, float &l, float x, float y) {
+    const float s = __fadd_rn(h, x), d = __fsub_rn(s, h);
+    const float e = __fadd_rn(__fadd_rn(__fsub_rn(h, __fsub_rn(s, d)), __fsub_rn(x, d)), __fadd_rn(l, y));
+    h = __fadd_rn(s, e);
+    l = __fsub_rn(e, __fsub_rn(h, s));
 }
 
 // The product fragments of 16 channels.  An A fragment holds two rows (lane
@@ -201,13 +212,13 @@ template <typename T, int D, int NP> struct Shape {
     static constexpr int kVRow = D + (sizeof(T) == 2 ? 8 : 4); // of a value row, later the output
     static constexpr int kA = NP, kP = NP + 8;                 // floats of a row of A and of P (then M)
     static constexpr size_t kv = 2 * NP * kRow * sizeof(T), ka = kv + NP * kVRow * sizeof(T), kp = ka + NP * kA * 4,
-                            kn = kp + NP * kP * 4, kBytes = kn + NP * (4 + 4 + 8 + 4);
+                            kn = kp + NP * kP * 4, kBytes = kn + NP * (8 + 4 + 4 + 4 + 4);
 };
 
 // CTAs of an SM.  Two hide one another's phases, which outweighs the spills that
 // their registers cost (64 sequences of 16 heads, d = 128, bf16: 47.1 -> 36.4 us
 // at 32 nodes, 94.0 -> 80.6 at 64; fp32 87 -> 73 at 32, now 78), except where every
-// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two (157 now).
+// fragment is held twice: fp32 at 64 nodes, 179 us with one and 233 with two (159 now).
 template <typename T, int D, int NP> constexpr int kPerSm = sizeof(T) == 4 && D == 128 && NP == 64 ? 1 : 2;
 
 template <typename T, int D, int NP>
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
     float *as = reinterpret_cast<float *>(sm + S::ka);        // [NP][kA]
     float *ps = reinterpret_cast<float *>(sm + S::kp);        // [NP][kP]
     unsigned long long *anc = reinterpret_cast<unsigned long long *>(sm + S::kn);   // [NP]
-    float *Gs = reinterpret_cast<float *>(anc + NP), *bs = Gs + NP;                 // [NP]
+    float *Gs = reinterpret_cast<float *>(anc + NP), *Gl = Gs + NP, *bs = Gl + NP;  // [NP]: G = Gs + Gl
     int *up = reinterpret_cast<int *>(bs + NP);                                      // [NP]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int b = blockIdx.x / L.H, h = blockIdx.x % L.H;
@@ -260,9 +271,11 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
     }
     if (!main_warp) {
         // ancestors and path sums by doubling: every round a node takes over
-        // what its current ancestor pointer has gathered
+        // what its current ancestor pointer has gathered.  G is a sum of two floats: one
+        // alone would leave the decays below a gate of -75 off by 2^-18 (4e-6 in the
+        // norm of the outputs), below one of -1e6 by 3 % and more.
         const int i = tid - 32 * S::kMain;
-        float G = 0.f;
+        float G = 0.f, G_low = 0.f;
         unsigned long long a = 0;
         int p = -1;
         if (i < NP) {
@@ -279,12 +292,13 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
         for (int round = 1; round < NP; round *= 2) {
             if (i < NP) {
                 Gs[i] = G;
+                Gl[i] = G_low;
                 anc[i] = a;
                 up[i] = p;
             }
             asm volatile("bar.sync 1, %0;" ::"r"(32 * S::kSolve) : "memory");
             if (p >= 0) {
-                G += Gs[p];
+                add_two(G, G_low, Gs[p], Gl[p]);
                 a |= anc[p];
                 p = up[p];
             }
@@ -292,6 +306,7 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
         }
         if (i < NP) {
             Gs[i] = G;
+            Gl[i] = G_low;
             anc[i] = a;
         }
     }
@@ -322,14 +337,14 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
                     F::mma_rows(c[s & 1], r0 + 16 * s, r1 + 16 * s, fb);
                 }
             }
-            const float2 Gj = *reinterpret_cast<const float2 *>(Gs + j0 + 2 * t);
+            const float2 Gj = *reinterpret_cast<const float2 *>(Gs + j0 + 2 * t), Gj_low = *reinterpret_cast<const float2 *>(Gl + j0 + 2 * t);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = i0 + g + 8 * e, j = j0 + 2 * t;
                 const unsigned two = (unsigned)(anc[i] >> j) & 3u;
-                const float G = Gs[i];
-                float x = two & 1 ? (c[0][2 * e] + c[1][2 * e]) * F::exp(G - Gj.x) : 0.f;
-                float y = two & 2 ? (c[0][2 * e + 1] + c[1][2 * e + 1]) * F::exp(G - Gj.y) : 0.f;
+                const float G = Gs[i], G_low = Gl[i];
+                float x = two & 1 ? (c[0][2 * e] + c[1][2 * e]) * F::exp((G - Gj.x) + (G_low - Gj_low.x)) : 0.f;
+                float y = two & 2 ? (c[0][2 * e + 1] + c[1][2 * e + 1]) * F::exp((G - Gj.y) + (G_low - Gj_low.y)) : 0.f;
                 if (!reads) {
                     const float be = bs[i];
                     x = j == i ? 0.f : x * be;
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(Shape<T, D, NP>::kThreads, kPerSm<T, D, NP>)
         if (i < NP) {
             float m[NP];
             // steps without a branch between them, so that the loads of the next run
-            // ahead: 15.8 -> 12.9 us for 24 fp32 trees of 33 nodes (12.6 now); at 32 nodes the
+            // ahead: 15.8 -> 12.9 us for 24 fp32 trees of 33 nodes (13.0 now); at 32 nodes the
             // registers this takes cost 2 %
             constexpr int kRun = NP == 64 ? 16 : 1;
             float *row = ps + i * S::kP;
