@@ -492,7 +492,9 @@ int gdn_tree_step(const void *q, const void *k, const void *v, const float *g, c
  *
  * A query whose lse is -infinity adds nothing.  With a window only keys within
  * it of the query count (positions as above; token j of a call is at seen[b] +
- * j).  The sum of a slot runs in a fixed order, so results repeat bit by bit.
+ * j).  scale, window, cache_pos and seen have to be those that lse was computed
+ * with: a key that lse leaves out has no bounded weight.  The sum of a slot
+ * runs in a fixed order, so results repeat bit by bit.
  *
  *   q            [total_queries, Hq, d]  bf16;   lse  [total_queries, Hq]  fp32
  *   k            [total_tokens, Hkv, d]  bf16

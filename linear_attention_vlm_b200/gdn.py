@@ -587,7 +587,8 @@ def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent
     parents [T] int32 (index in the sequence, -1 at a root) or None for chains;
     k_cache, v_cache [B, capacity, Hkv, 128]; cache_lens [B] int32;
     cu_seqlens int32 [B+1] or None (equal trees).  ``max_nodes`` bounds the
-    nodes of one sequence (default min(T, 64); a tighter bound costs less).
+    nodes of one sequence (default min(T, 64); a tighter bound costs less; the
+    rows of a sequence from the bound on are not written).
     With cache_pos [B, Hkv, capacity] and seen [B] (int32) the window goes by
     token positions.  Returns (o [T, Hq, 128], lse [T, Hq] fp32)."""
     T, Hq, d = q.shape
@@ -635,8 +636,8 @@ def gdn_tree_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     """Read-out of every node of a tree of drafted tokens from one state per
     sequence, which stays as it is (include/gdn.h, gdn_tree_step).  q, k, v
     [T, H, d]; g, beta [T, H] fp32; parents [T] int32 or None for chains; state
-    [B, H, d, d] fp32; cu_seqlens int32 [B+1] or None (equal trees).  Returns
-    out [T, H, d]."""
+    [B, H, d, d] fp32; cu_seqlens int32 [B+1] or None (equal trees);
+    ``max_nodes`` as in gdn_tree_attention.  Returns out [T, H, d]."""
     T, H, d = q.shape
     dev, dt = q.device, q.dtype
     if dev.type != "cuda":
@@ -681,9 +682,10 @@ def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cac
     """Attention weight per cache slot, added up (include/gdn.h,
     gdn_cache_weights).  q [Tq, Hq, 128] bf16 and lse [Tq, Hq] fp32 of the last
     queries of the new tokens, whose keys are k [T, Hkv, 128]; k_cache
-    [B, capacity, Hkv, 128]; weights [B, Hkv, capacity] fp32.  ``weights_out``
-    defaults to ``weights`` (in place).  Returns (weights_out, new_weights
-    [T, Hkv] fp32)."""
+    [B, capacity, Hkv, 128]; weights [B, Hkv, capacity] fp32.  ``cache_pos``,
+    ``seen``, ``window`` and ``scale`` as in the call that returned lse.
+    ``weights_out`` defaults to ``weights`` (in place).  Returns (weights_out,
+    new_weights [T, Hkv] fp32)."""
     Tq, Hq, d = q.shape
     T = k.shape[0]
     dev, dt = q.device, q.dtype
