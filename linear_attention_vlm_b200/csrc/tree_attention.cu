@@ -291,8 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // total units, then the sequence that this CTA's run starts in
     int64_t *plan = reinterpret_cast<int64_t *>(ctl + kOffPlan);                // units before the first sequence, its index
     Seq *plan_seq = reinterpret_cast<Seq *>(plan + 2);
-    int64_t *wsum = reinterpret_cast<int64_t *>(sm);                            // [11] scratch before any copy lands
+    int64_t *wsum = reinterpret_cast<int64_t *>(ctl + kOffXch);                 // [11], where no copy (async proxy) ever lands
     static_assert(16 + sizeof(Seq) <= kOffPar - kOffPlan, "plan area");
+    static_assert(kOffXch % 8 == 0 && 8 * kThreads / 32 <= kCtlBytes - kOffXch, "scratch of the plan");
     int64_t W = 0, w0 = 0, w1 = 0;
     const bool one_pass = p.num_seqs <= kThreads;
     if (!one_pass) {   // the total first
