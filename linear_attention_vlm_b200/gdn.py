@@ -536,6 +536,14 @@ def _opt(what: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, dev) -
     return None if t is None else _arg(what, t, shape, dtype, dev)
 
 
+def _int32(what: str, x: int) -> int:
+    """``x`` for a C int, which ctypes would cut to its low 32 bits."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError("%s must fit 32 bits, got %d" % (what, x))
+    return x
+
+
 def _scratch(workspace: Optional[torch.Tensor], need: int, dev) -> Tuple[torch.Tensor, int]:
     if workspace is None:
         return torch.empty(need or 16, dtype=torch.uint8, device=dev), need
@@ -551,7 +559,7 @@ def _current(dev):
 
 def _tree_nodes(max_nodes: Optional[int], cu: Optional[torch.Tensor], T: int, B: int) -> int:
     if max_nodes is not None:
-        return int(max_nodes)
+        return _int32("max_nodes", max_nodes)
     return max(1, min(MAX_TREE_NODES, T)) if cu is not None else max(1, T // max(B, 1))
 
 
@@ -617,7 +625,7 @@ def gdn_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parent
         _arg("v_cache", v_cache, old, dt, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
         _opt("cache_pos", cache_pos, (B, Hkv, cap), i32, dev), _opt("seen", seen, (B,), i32, dev),
         o_at, lse_at, B, T, n, cap, Hq, Hkv, d,
-        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
+        _int32("window", window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
         _stream(dev))
     guard = _current(dev)
     if guard is None:
@@ -708,7 +716,7 @@ def gdn_cache_weights(q: torch.Tensor, lse: torch.Tensor, k: torch.Tensor, k_cac
         new_at, _opt("cu_queries", cu_queries, (B + 1,), i32, dev),
         _opt("cu_tokens", cu_tokens, (B + 1,), i32, dev), _arg("cache_lens", cache_lens, (B,), i32, dev),
         _opt("cache_pos", cache_pos, cells, i32, dev), _opt("seen", seen, (B,), i32, dev), B, Tq, T, cap, Hq, Hkv, d,
-        int(window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
+        _int32("window", window), 0.0 if scale is None else float(scale), code, ws.data_ptr(), ws_bytes,
         _stream(dev))
     guard = _current(dev)
     if guard is None:
@@ -762,7 +770,7 @@ def gdn_cache_insert(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
         ln, ln if lens_out is None else _arg("lens_out", lens_out, (B,), i32, dev),
         sn, sn if seen_out is None else _arg("seen_out", seen_out, (B,), i32, dev),
         _opt("new_weights", new_weights, (T, Hkv), f32, dev), slots_at,
-        _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, cap, Hkv, d, int(recent), code, ws.data_ptr(),
+        _opt("cu_seqlens", cu_seqlens, (B + 1,), i32, dev), B, T, cap, Hkv, d, _int32("recent", recent), code, ws.data_ptr(),
         ws_bytes,
         _stream(dev))
     guard = _current(dev)
