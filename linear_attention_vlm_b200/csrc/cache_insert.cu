@@ -408,6 +408,9 @@ cudaError_t launch_cache_insert(const CacheInsertLaunch &L, cudaStream_t stream)
     // 8192 slots of 2 heads of 128 in bf16: 19.0 against 19.8 us for 64
     // sequences of 4 tokens, 45 against 55 of 1024; one sequence of 1 token 19.0
     // against 19.5, of 256 23.3 against 20.0.  A launch less is 2 us of the host.
+    // The lengths of the lists are not known here, only their mean: a list far above it is
+    // left to one CTA a head (one of 16384 tokens among 63 of one token takes
+    // 195 us, alone 30).
     const int64_t list_bytes = 2 * (L.total_tokens / L.num_seqs) * L.row_bytes;
     const bool whole = ctas == 1 && L.Hkv <= kMaxCluster &&
                        (list_bytes <= kWholeBytes || 2 * (int64_t)L.num_seqs * L.Hkv >= kSMs);

@@ -10,9 +10,12 @@
 // holds the tree's own keys, masked by the ancestor bits of each node; a cache's
 // last block ends inside the tile.
 //
-// What bounds it: K and V are read once, 512 bytes a slot and key/value head,
-// against 512 Hq / Hkv n flops: memory up to about n Hq / Hkv = 260 rows, the
-// tensor pipe above.  So the work is cut by keys, not by rows: all (sequence,
+// What bounds it: K and V, 512 bytes a slot and key/value head, against 512 Hq /
+// Hkv n flops: memory up to about n Hq / Hkv = 260 rows, the tensor pipe above.
+// An item has at most 256 rows, so up to there K and V are read once, and again
+// for every further 256: 32 trees of 32 to 64 nodes (256 to 512 rows a head) at
+// 8192 slots read 428 MB from memory where 279 would do; at 66 us of copy rate
+// that is not what bounds their 167.  So the work is cut by keys, not by rows: all (sequence,
 // key/value head, row tiles) items are laid end to end as key blocks and every
 // CTA takes an equal run of them, whatever the lengths; an item that crosses
 // CTAs leaves partial sums that a second kernel joins.

@@ -17,8 +17,9 @@
 // queries are read in the same order of channels, so no shuffle or shared
 // memory is needed for S.  The result fragments (value channel x node) are the
 // A fragments of the second product, with M: nothing of size n x d leaves the
-// registers between them.  tcgen05 would want S as bf16 pairs in shared memory
-// and twice the passes through it for products this small (n <= 64 columns).
+// registers between them.  (tcgen05, with S as bf16 pairs in tensor memory and the rows of
+// keys and queries read once instead of by every warp, is not built: it would serve
+// the larger trees.)
 // With d = 128 in bf16, 64 sequences of 16 heads (67 MB of state) take 19.1 us
 // at 4 nodes and 21.6 at 16 (3.7 TB/s with the rows); at 64 nodes 78, where
 // the chain of the substitution (64 steps in two warps) and the products that
