@@ -36,7 +36,6 @@ constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kKeep = 10;          // keys a thread holds: 10240 candidates a CTA; the rest are read again
 constexpr int kRowsAhead = 4;      // rows of a warp in flight
 constexpr int64_t kWholeBytes = 64 << 10;
-constexpr int kSMs = 148;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;     // the portable limit
 constexpr unsigned kAll = 0xffffffffu;
@@ -395,6 +394,15 @@ size_t cache_insert_workspace(int64_t total_tokens, int Hkv) {
 }
 
 cudaError_t launch_cache_insert(const CacheInsertLaunch &L, cudaStream_t stream) {
+    static int sms[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!sms[dev]) {
+        e = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
     const int64_t uniform_len = L.cu_seqlens ? 0 : L.total_tokens / L.num_seqs;
     // a cluster per (sequence, head) where its candidates, at the sequences'
     // mean, are more than one CTA keeps
@@ -413,7 +421,7 @@ cudaError_t launch_cache_insert(const CacheInsertLaunch &L, cudaStream_t stream)
     // 195 us, alone 30).
     const int64_t list_bytes = 2 * (L.total_tokens / L.num_seqs) * L.row_bytes;
     const bool whole = ctas == 1 && L.Hkv <= kMaxCluster &&
-                       (list_bytes <= kWholeBytes || 2 * (int64_t)L.num_seqs * L.Hkv >= kSMs);
+                       (list_bytes <= kWholeBytes || 2 * (int64_t)L.num_seqs * L.Hkv >= sms[dev]);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(L.num_seqs * L.Hkv * ctas));
     cfg.blockDim = dim3(kSelThreads);
@@ -424,7 +432,7 @@ cudaError_t launch_cache_insert(const CacheInsertLaunch &L, cudaStream_t stream)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, cache_select_kernel, L, uniform_len, ctas, whole);
+    e = cudaLaunchKernelEx(&cfg, cache_select_kernel, L, uniform_len, ctas, whole);
     if (e != cudaSuccess || whole) return e;
     int64_t x = (L.total_tokens * L.Hkv / L.num_seqs + kCopyWarps - 1) / kCopyWarps;
     x = x < 1 ? 1 : x > 4096 ? 4096 : x;
