@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (mine) {
                         if (!old) kp = key;
                         else
-                            kp = (int)max((int64_t)INT32_MIN / 2, min((int64_t)(s.m - s.nq), (p.pos ? (int64_t)p.pos[slot] : key) - seen));
+                            kp = (int)max((int64_t)INT32_MIN, min((int64_t)(s.m - s.nq), (p.pos ? (int64_t)p.pos[slot] : key) - seen));
                     }
                     all = false;
                 }
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 const float e = ex2_approx(fmaf(v[i], c2, -ls[c0 + i]));
-                                a[i & 3] += (uint32_t)(ps[c0 + i] - kp) < (uint32_t)p.window ? e : 0.f;
+                                a[i & 3] += (uint32_t)ps[c0 + i] - (uint32_t)kp < (uint32_t)p.window ? e : 0.f;   // a distance below 0 is above 2^31
                             }
                         }
                         sum += (a[0] + a[1]) + (a[2] + a[3]);
