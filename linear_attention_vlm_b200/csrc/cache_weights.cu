@@ -15,8 +15,8 @@
 // and SM against 32 keys' worth of tensor work).
 //
 // Bf16, 16 query and 2 key/value heads: 5 queries of each of 32 sequences over 0 to
-// 8192 slots take 29.5 us (3.6 TB/s), 64 queries over the 32768 tokens of a prompt
-// 22.9 (8.5 us of exponentials at 16 a clock).
+// 8192 slots take 28.9 us (3.6 TB/s), 64 queries over the 32768 tokens of a prompt
+// 22.8 (8.5 us of exponentials at 16 a clock).
 //
 // All (sequence, key/value head, key block) units are laid end to end, each
 // weighted by its row chunks, and cut evenly over one persistent CTA per SM.

@@ -15,7 +15,7 @@
 // An item has at most 256 rows, so up to there K and V are read once, and again
 // for every further 256: 32 trees of 32 to 64 nodes (256 to 512 rows a head) at
 // 8192 slots read 428 MB from memory where 279 would do; at 66 us of copy rate
-// that is not what bounds their 167.  So the work is cut by keys, not by rows: all (sequence,
+// that is not what bounds their 166.  So the work is cut by keys, not by rows: all (sequence,
 // key/value head, row tiles) items are laid end to end as key blocks and every
 // CTA takes an equal run of them, whatever the lengths; an item that crosses
 // CTAs leaves partial sums that a second kernel joins.
@@ -38,9 +38,9 @@
 //                     waits and issues (about 3000 cycles per half block) were
 //                     longer than the products and the softmax (1200 each)
 // Bandwidth and rates reached, bf16, 16 query and 2 key/value heads: a token of 64
-// sequences at 0 to 8192 slots 57 us (4.6 TB/s, of which 13 us are the first
-// copies, the merge and the join); 24 nodes at 262144 slots 83 us (3.2 TB/s, 0.6
-// PFLOP/s); 32 trees of 64 nodes at 8192 slots 167 us.  With many rows the hand-over
+// sequences at 0 to 8192 slots 59 us (4.4 TB/s, of which 13 us are the first
+// copies, the merge and the join); 24 nodes at 262144 slots 84 to 91 us by the box
+// (2.9 to 3.2 TB/s, 0.6 PFLOP/s); 32 trees of 64 nodes at 8192 slots 166 us.  With many rows the hand-over
 // between softmax and products of a stream bounds it: a half block takes 2050
 // cycles, 1350 of them the exponentials and the conversions of 128 rows x 64 keys
 // a stream (the special-function units alone need 1100 for two streams).
